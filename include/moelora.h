@@ -214,6 +214,127 @@ MOELORA_API moelora_status moelora_forward_noalloc(moelora_plan_t plan, int32_t 
                                const void *lora_a_d, const void *lora_b_d,
                                void *out, moelora_stream_t stream);
 
+/* ---------------------------------------------------------------------
+ * Stand-alone operators: the layer's steps for callers that put their own
+ * expert function, gradients or block-scaled FP8 weights between them.
+ *
+ * Common rules.  Row-major, contiguous; every device pointer 16-byte
+ * aligned and on the current device; each call enqueues on `stream`,
+ * allocates nothing, synchronises nothing and keeps nothing, so it can be
+ * captured in a HIP graph.  Inputs and outputs must not overlap.  Results
+ * repeat bit for bit (no floating-point atomics), sums run in float32 and are
+ * rounded once.  dtype is MOELORA_F32 or MOELORA_BF16 (else
+ * MOELORA_ERR_UNSUPPORTED).  The first call on a device loads the code of
+ * all of these operators.
+ *
+ * Token order.  T tokens, k experts each, R = T k routed rows p = t k + j.
+ * Limits (else MOELORA_ERR_UNSUPPORTED): 1 <= hidden <= 65536, 1 <= E <=
+ * 1024, 1 <= k <= 32, R <= 2^24.  k may exceed E: a shard that holds some of
+ * the experts numbers those 0 .. E-1 and marks rows of the others with any
+ * id outside [0, E) (say -1); such rows are dropped.
+ *
+ * moelora_dispatch sorts the routed rows by expert, stably (ascending p
+ * inside an expert), and copies their tokens into that order:
+ *   expert_start [E+1]  first sorted position of each expert's rows;
+ *                       expert_start[E] = rows kept
+ *   sorted_rows  [R]    routed row p at each sorted position, R past the
+ *                       rows kept
+ *   row_pos      [T][k] sorted position of each routed row, -1 if dropped
+ *   xs           [R][H] x[sorted_rows[pos] / k]; rows past the rows kept
+ *                       are left as they were.  NULL (x may be NULL
+ *                       too): the order only.
+ * workspace: moelora_dispatch_workspace bytes (0 for small batches, at
+ * most 1024 E), no initialisation.  n_tokens = 0 writes expert_start
+ * (zeros) and reads nothing. */
+MOELORA_API moelora_status moelora_dispatch_workspace(int32_t n_tokens, int32_t n_experts,
+                               int32_t top_k, size_t *workspace_bytes);
+MOELORA_API moelora_status moelora_dispatch(int32_t n_tokens, int32_t hidden, int32_t n_experts,
+                               int32_t top_k, int32_t dtype, const void *x,
+                               const int32_t *topk_ids, int32_t *expert_start,
+                               int32_t *sorted_rows, int32_t *row_pos, void *xs,
+                               void *workspace, size_t workspace_bytes,
+                               moelora_stream_t stream);
+
+/* Gradient of the copy: dx[t] = sum_j dxs[row_pos[t][j]], ascending j; a
+ * dropped row adds nothing.  row_pos entries outside [0, R) count as
+ * dropped here and in the calls below.  dxs [R][H], dx [T][H]. */
+MOELORA_API moelora_status moelora_dispatch_backward(int32_t n_tokens, int32_t hidden,
+                               int32_t top_k, int32_t dtype, const void *dxs,
+                               const int32_t *row_pos, void *dx,
+                               moelora_stream_t stream);
+
+/* out[t] = sum_j topk_w[t][j] ys[row_pos[t][j]], ascending j.  ys [R][H],
+ * topk_w [T][k] float32, out [T][H] (zeros where every row was dropped). */
+MOELORA_API moelora_status moelora_combine(int32_t n_tokens, int32_t hidden, int32_t top_k,
+                               int32_t dtype, const void *ys, const int32_t *row_pos,
+                               const float *topk_w, void *out, moelora_stream_t stream);
+
+/* Gradients of moelora_combine, given dout [T][H]:
+ *   dys [R][H]  dys[row_pos[t][j]] = topk_w[t][j] dout[t]; rows that no
+ *               routed row points to are left as they were.  NULL: not wanted
+ *               (topk_w may then be NULL).
+ *   dw [T][k]   float32, <dout[t], ys[row_pos[t][j]]>, 0 for a dropped row.
+ *               NULL: not wanted (ys may then be NULL).  */
+MOELORA_API moelora_status moelora_combine_backward(int32_t n_tokens, int32_t hidden,
+                               int32_t top_k, int32_t dtype, const void *dout,
+                               const void *ys, const int32_t *row_pos,
+                               const float *topk_w, void *dys, float *dw,
+                               moelora_stream_t stream);
+
+/* Block-scaled E4M3.  A row of `width` = K elements is stored as one code a
+ * byte, padded with zero bytes to the pitch P = round_up(K, 128), and one
+ * float32 scale per block of 128: value = scale * code.  KB = P / 128.
+ *   rows     codes [M][P], scales [KB][M] (block-major)
+ *   weights  codes [mats][N][P], scales [mats][NB][KB], one per 128 x 128
+ *            block, NB = ceil(N / 128)
+ * The quantisers choose the smallest power of two 2^e >= max|v| / 448 (e >=
+ * -126) of the block's finite elements as its scale and round v / 2^e, which
+ * is exact, to the nearest code, ties to even; an element that is not finite
+ * gets the NaN code.  The product takes any float32 scales.
+ * Limits (else MOELORA_ERR_UNSUPPORTED): 1 <= K <= 65536, rows of x <=
+ * 2^24, 1 <= N <= 131072, mats <= 65535, E <= 1024. */
+
+/* Rows r of x (rows = NULL; then n_src >= n_rows and row_div = 1), or rows
+ * rows[r] / row_div of the n_src rows of x: with the sorted_rows of
+ * moelora_dispatch and row_div = k the tokens in expert order.  Where
+ * rows[r] is negative or points past n_src (the tail of sorted_rows does),
+ * row r of codes and scales is left as it was. */
+MOELORA_API moelora_status moelora_quantize_rows(int32_t n_rows, int32_t width, int32_t dtype,
+                               const void *x, int32_t n_src, const int32_t *rows,
+                               int32_t row_div, void *codes, float *scales,
+                               moelora_stream_t stream);
+
+/* Weights w [mats][N][K].  codes_t, scales_t (both or neither): the same
+ * codes transposed, [mats][K][round_up(N, 128)] and [mats][KB][NB], the
+ * weights of the product's gradient in its rows: with dy [M][N] quantised by
+ * rows, dx = moelora_fp8_gemm of dy and (codes_t, scales_t), n_out = K,
+ * width = N. */
+MOELORA_API moelora_status moelora_quantize_weights(int32_t n_mats, int32_t rows,
+                               int32_t width, int32_t dtype, const void *w, void *codes,
+                               float *scales, void *codes_t, float *scales_t,
+                               moelora_stream_t stream);
+
+/* The grouped product: for the rows m of expert e, expert_start[e] <= m <
+ * expert_start[e+1],
+ *   out[m][n] = sum_b scales[b][m] w_scales[e][n/128][b]
+ *               sum_{k in block b} codes[m][k] w_codes[e][n][k]
+ * in float32, rounded once to out_dtype (MOELORA_F32, MOELORA_BF16), out
+ * [M][N].  For MOELORA_BF16 the FP8 matrix core forms the sums over a block,
+ * which are off by at most 7 2^-13 of the block's sum of magnitudes (on
+ * normal data 1.5e-5 of the result); for MOELORA_F32 the products are exact
+ * and summed in float32.  Rows outside every expert's range are left as they were.
+ * expert_start = NULL with n_experts = 1: all rows (a dense product).
+ * Entries of expert_start are clamped into [0, M]; they must not fall.
+ * With MOELORA_FP8_SILU_MUL the weights of an expert are two matrices, gate
+ * then up (w_codes [E][2][N][P], w_scales [E][2][NB][KB]: mats = 2 E), and
+ * out = SiLU(gate) * up. */
+#define MOELORA_FP8_SILU_MUL 1u
+MOELORA_API moelora_status moelora_fp8_gemm(int32_t n_rows, int32_t n_out, int32_t width,
+                               int32_t n_experts, int32_t out_dtype, uint32_t flags,
+                               const void *codes, const float *scales,
+                               const int32_t *expert_start, const void *w_codes,
+                               const float *w_scales, void *out, moelora_stream_t stream);
+
 MOELORA_API const char *moelora_status_string(moelora_status status);
 
 /* ---------------------------------------------------------------------

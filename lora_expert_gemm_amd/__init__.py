@@ -42,6 +42,7 @@ STATIC_SCRATCH_BYTES = 64 << 20
 F32, BF16, BF16_FP8W = 0, 1, 2
 DEVERR_EXPERT_ID, DEVERR_ADAPTER_ID = 1, 2
 FLAG_DETERMINISTIC, FLAG_DEBUG_CHECK_IDS = 1, 2
+FP8_SILU_MUL = 1
 N_STAGES = 6
 STAGES = ("route_align", "shrink_gate_up", "gate_up", "shrink_down", "down", "combine")
 
@@ -87,6 +88,18 @@ _lib.moelora_timing_begin.restype = ctypes.c_int
 _lib.moelora_timing_end.argtypes = [_P, ctypes.POINTER(ctypes.c_double), _I32,
                                     ctypes.POINTER(_I32)]
 _lib.moelora_timing_end.restype = ctypes.c_int
+_U32 = ctypes.c_uint32
+_lib.moelora_dispatch_workspace.argtypes = [_I32] * 3 + [ctypes.POINTER(ctypes.c_size_t)]
+_lib.moelora_dispatch.argtypes = [_I32] * 5 + [_P] * 7 + [ctypes.c_size_t, _P]
+_lib.moelora_dispatch_backward.argtypes = [_I32] * 4 + [_P] * 4
+_lib.moelora_combine.argtypes = [_I32] * 4 + [_P] * 5
+_lib.moelora_combine_backward.argtypes = [_I32] * 4 + [_P] * 7
+_lib.moelora_quantize_rows.argtypes = [_I32] * 3 + [_P, _I32, _P, _I32] + [_P] * 3
+_lib.moelora_quantize_weights.argtypes = [_I32] * 4 + [_P] * 6
+_lib.moelora_fp8_gemm.argtypes = [_I32] * 5 + [_U32] + [_P] * 7
+for _n in ("dispatch_workspace", "dispatch", "dispatch_backward", "combine", "combine_backward",
+           "quantize_rows", "quantize_weights", "fp8_gemm"):
+    getattr(_lib, "moelora_" + _n).restype = ctypes.c_int
 
 
 def fp8_weight_buffer(codes, scales):
@@ -141,7 +154,7 @@ def exported_symbols():
     """Names of the functions include/moelora.h declares."""
     with open(HEADER_PATH) as f:
         text = f.read()
-    return sorted(set(re.findall(r"\b(moelora_[a-z_]+)\s*\(", text)))
+    return sorted(set(re.findall(r"\b(moelora_[a-z0-9_]+)\s*\(", text)))
 
 
 def moelora_status_string(status):
@@ -214,6 +227,110 @@ def moelora_timing_end(plan):
     n = _I32()
     _check(_lib.moelora_timing_end(plan, ms, N_STAGES, ctypes.byref(n)), "moelora_timing_end")
     return list(ms), n.value
+
+
+# ---- stand-alone operators.  A tensor argument is checked before its address
+# is passed on: contiguous, on the current device, elements of the expected
+# size and at least as many as the call reads or writes.
+
+def _buf(t, n, size, name, optional=False):
+    if t is None:
+        if optional or n == 0:
+            return None
+        raise ValueError(f"{name} is required")
+    if isinstance(t, int):
+        return t
+    if t.numel() < n or t.element_size() != size or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor of at least {n} elements of "
+                         f"{size} bytes, got {tuple(t.shape)} {t.dtype} strides {t.stride()}")
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
+    return t.data_ptr()
+
+
+def _es(dtype):
+    return 4 if dtype == F32 else 2
+
+
+def moelora_dispatch_workspace(n_tokens, n_experts, top_k):
+    """-> workspace bytes of moelora_dispatch."""
+    n = ctypes.c_size_t()
+    _check(_lib.moelora_dispatch_workspace(n_tokens, n_experts, top_k, ctypes.byref(n)),
+           "moelora_dispatch_workspace")
+    return n.value
+
+
+def moelora_dispatch(n_tokens, hidden, n_experts, top_k, dtype, x, topk_ids, expert_start,
+                     sorted_rows, row_pos, xs, workspace, workspace_bytes, stream=None):
+    R, es = n_tokens * top_k, _es(dtype)
+    _check(_lib.moelora_dispatch(
+        n_tokens, hidden, n_experts, top_k, dtype,
+        _buf(x, n_tokens * hidden, es, "x", xs is None), _buf(topk_ids, R, 4, "topk_ids"),
+        _buf(expert_start, n_experts + 1, 4, "expert_start"),
+        _buf(sorted_rows, R, 4, "sorted_rows"), _buf(row_pos, R, 4, "row_pos"),
+        _buf(xs, R * hidden, es, "xs", True),
+        _buf(workspace, workspace_bytes, 1, "workspace", True), workspace_bytes,
+        _stream(stream)), "moelora_dispatch")
+
+
+def moelora_dispatch_backward(n_tokens, hidden, top_k, dtype, dxs, row_pos, dx, stream=None):
+    R, es = n_tokens * top_k, _es(dtype)
+    _check(_lib.moelora_dispatch_backward(
+        n_tokens, hidden, top_k, dtype, _buf(dxs, R * hidden, es, "dxs"),
+        _buf(row_pos, R, 4, "row_pos"), _buf(dx, n_tokens * hidden, es, "dx"), _stream(stream)),
+        "moelora_dispatch_backward")
+
+
+def moelora_combine(n_tokens, hidden, top_k, dtype, ys, row_pos, topk_w, out, stream=None):
+    R, es = n_tokens * top_k, _es(dtype)
+    _check(_lib.moelora_combine(
+        n_tokens, hidden, top_k, dtype, _buf(ys, R * hidden, es, "ys"),
+        _buf(row_pos, R, 4, "row_pos"), _buf(topk_w, R, 4, "topk_w"),
+        _buf(out, n_tokens * hidden, es, "out"), _stream(stream)), "moelora_combine")
+
+
+def moelora_combine_backward(n_tokens, hidden, top_k, dtype, dout, ys, row_pos, topk_w, dys, dw,
+                             stream=None):
+    R, es = n_tokens * top_k, _es(dtype)
+    _check(_lib.moelora_combine_backward(
+        n_tokens, hidden, top_k, dtype, _buf(dout, n_tokens * hidden, es, "dout"),
+        _buf(ys, R * hidden, es, "ys", dw is None), _buf(row_pos, R, 4, "row_pos"),
+        _buf(topk_w, R, 4, "topk_w", dys is None), _buf(dys, R * hidden, es, "dys", True),
+        _buf(dw, R, 4, "dw", True), _stream(stream)), "moelora_combine_backward")
+
+
+def moelora_quantize_rows(n_rows, width, dtype, x, n_src, rows, row_div, codes, scales,
+                          stream=None):
+    kb = (width + 127) // 128
+    _check(_lib.moelora_quantize_rows(
+        n_rows, width, dtype, _buf(x, n_src * width, _es(dtype), "x"), n_src,
+        _buf(rows, n_rows, 4, "rows", True), row_div, _buf(codes, n_rows * kb * 128, 1, "codes"),
+        _buf(scales, n_rows * kb, 4, "scales"), _stream(stream)), "moelora_quantize_rows")
+
+
+def moelora_quantize_weights(n_mats, rows, width, dtype, w, codes, scales, codes_t=None,
+                             scales_t=None, stream=None):
+    kb, nb = (width + 127) // 128, (rows + 127) // 128
+    _check(_lib.moelora_quantize_weights(
+        n_mats, rows, width, dtype, _buf(w, n_mats * rows * width, _es(dtype), "w"),
+        _buf(codes, n_mats * rows * kb * 128, 1, "codes"),
+        _buf(scales, n_mats * nb * kb, 4, "scales"),
+        _buf(codes_t, n_mats * width * nb * 128, 1, "codes_t", True),
+        _buf(scales_t, n_mats * nb * kb, 4, "scales_t", True), _stream(stream)),
+        "moelora_quantize_weights")
+
+
+def moelora_fp8_gemm(n_rows, n_out, width, n_experts, out_dtype, flags, codes, scales,
+                     expert_start, w_codes, w_scales, out, stream=None):
+    kb, nb = (width + 127) // 128, (n_out + 127) // 128
+    mats = n_experts * (2 if flags & FP8_SILU_MUL else 1)
+    _check(_lib.moelora_fp8_gemm(
+        n_rows, n_out, width, n_experts, out_dtype, flags,
+        _buf(codes, n_rows * kb * 128, 1, "codes"), _buf(scales, n_rows * kb, 4, "scales"),
+        _buf(expert_start, n_experts + 1, 4, "expert_start", True),
+        _buf(w_codes, mats * n_out * kb * 128, 1, "w_codes"),
+        _buf(w_scales, mats * nb * kb, 4, "w_scales"),
+        _buf(out, n_rows * n_out, _es(out_dtype), "out"), _stream(stream)), "moelora_fp8_gemm")
 
 
 class Plan:

@@ -17,7 +17,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIB_DIR, "libmoelora.so")
-SOURCES = ["api.hip", "align.hip", "expert_gemm.hip", "tiled_gemm.hip"]
+SOURCES = ["api.hip", "align.hip", "expert_gemm.hip", "tiled_gemm.hip",
+           "ops_api.hip", "token_order.hip", "block_fp8.hip", "fp8_gemm.hip"]
 ARCH = "gfx950"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
@@ -32,7 +33,7 @@ FLAGS = [
 # Sources whose GEMM kernels wait on counts of their own vector-memory loads
 # (s_waitcnt vmcnt with a fixed immediate): a scratch spill reload is a
 # vector load too, so every kernel of these must use no scratch memory.
-COUNTED_WAITS = ("expert_gemm.hip", "tiled_gemm.hip")
+COUNTED_WAITS = ("expert_gemm.hip", "tiled_gemm.hip", "fp8_gemm.hip")
 # The device assembly of the streaming GEMMs is kept for the CPU test that
 # checks the compiled weight-ring loops against their wait counts.
 ASM_SOURCES = ("expert_gemm.hip",)

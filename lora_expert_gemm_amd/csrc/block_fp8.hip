@@ -1,0 +1,226 @@
+// Quantisation to OCP E4M3 with one scale per block of 128 along the
+// contraction (rows) or per block of 128 x 128 (weights).
+//
+// The scale of a block is a power of two, the smallest 2^e with
+// max|v| / 448 <= 2^e (448: the format's largest value; e >= -126), taken
+// from the bits of max|v|.  v / 2^e is then exact in float32, so a code is
+// one rounding of the input itself (nearest, ties to even) and no value sits
+// on a border that depends on how a division was rounded; the price is up to
+// one bit of the block's head room, which a floating-point code does not
+// feel.  Elements that are not finite get the NaN code and do not count in
+// max|v|.  Bound by HBM: every input is read once (a lane converts eight
+// consecutive elements from registers), a code and 1/32 byte of scale are
+// written per element.
+#include "common.h"
+#include "kernels.h"
+#include "ops.h"
+
+namespace moelora {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kBlk = 128;    // elements a scale
+constexpr int kLanes = 16;   // lanes on a block, 8 elements each
+constexpr int kGroups = kThreads / kLanes;
+
+// Eight elements of a row of K from element c on, zeros past K.
+template <typename DT, bool VEC>
+__device__ __forceinline__ void load8(const DT *row, int c, int K, float *f) {
+  if constexpr (VEC && sizeof(DT) == 2) {
+    u32x4_t v = c < K ? *reinterpret_cast<const u32x4_t *>(row + c) : u32x4_t{0, 0, 0, 0};
+    const Chunk<uint16_t> h = chunk_elems<uint16_t>(v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = bf16_to_f32(h.v[i]);
+  } else if constexpr (VEC) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const f32x4_t v = c + 4 * q < K ? *reinterpret_cast<const f32x4_t *>(row + c + 4 * q)
+                                      : f32x4_t{0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[4 * q + i] = v[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = c + i < K ? Elem<DT>::to_f32(row[c + i]) : 0.f;
+  }
+}
+
+// Largest finite magnitude, as the bits of a non-negative float.
+__device__ __forceinline__ uint32_t amax_bits8(const float *f) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t b = __float_as_uint(f[i]) & 0x7fffffffu;
+    m = max(m, b < 0x7f800000u ? b : 0u);
+  }
+  return m;
+}
+
+// e of the block's scale 2^e: amax = (1 + m) 2^q gives amax / 448 <= 2^(q - 8)
+// exactly when 1 + m <= 1.75.
+__device__ __forceinline__ int scale_exp(uint32_t amax) {
+  const int q = (int)(amax >> 23) - 127;
+  return max(-126, q - 8 + ((amax & 0x7fffffu) > 0x600000u));
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+
+__device__ __forceinline__ uint32_t codes4(const float *f, float inv) {
+  float g[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) g[i] = f[i] * inv;
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(g[0], g[1], 0, false);
+  w = __builtin_amdgcn_cvt_pk_fp8_f32(g[2], g[3], w, true);
+  uint32_t u = (uint32_t)w;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if ((__float_as_uint(f[i]) & 0x7fffffffu) >= 0x7f800000u)
+      u = (u & ~(0xffu << 8 * i)) | (0x7fu << 8 * i);
+  return u;
+}
+
+// 16 rows a workgroup, up to kUnroll blocks of each: 16 lanes a (row, block).
+// The blocks' loads are all issued before the first is used; the rows'
+// scales of one block are neighbours in memory.
+constexpr int kUnroll = 4;
+template <typename DT, bool VEC>
+__global__ __launch_bounds__(kThreads) void k_quant_rows(QuantRowsArgs a, int KB, int per_wg) {
+  const int g = threadIdx.x / kLanes, l = threadIdx.x % kLanes;
+  const int r = blockIdx.x * kGroups + g;
+  if (r >= a.M) return;
+  int src = r;
+  if (a.rows) {
+    const int p = a.rows[r];
+    src = p < 0 ? -1 : p / a.div;
+    if ((unsigned)src >= (unsigned)a.n_src) return;  // whole group: its row is left as it was
+  }
+  const DT *row = static_cast<const DT *>(a.x) + (size_t)src * a.K;
+  uint8_t *out = a.codes + (size_t)r * KB * kBlk;
+  const int b_end = min(KB, ((int)blockIdx.y + 1) * per_wg);
+  for (int b0 = blockIdx.y * per_wg; b0 < b_end; b0 += kUnroll) {
+    float f[kUnroll][8];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+      if (b0 + u < b_end) load8<DT, VEC>(row, (b0 + u) * kBlk + l * 8, a.K, f[u]);
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      if (b0 + u >= b_end) break;
+      uint32_t m = amax_bits8(f[u]);
+#pragma unroll
+      for (int d = 1; d < kLanes; d <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
+      const int e = scale_exp(m);
+      const float inv = pow2(-e);
+      const uint2 c = make_uint2(codes4(f[u], inv), codes4(f[u] + 4, inv));
+      *reinterpret_cast<uint2 *>(out + (size_t)(b0 + u) * kBlk + l * 8) = c;
+      if (l == 0) a.scales[(size_t)(b0 + u) * a.M + r] = pow2(e);
+    }
+  }
+}
+
+// One 128 x 128 block a workgroup, held in registers between the maximum and
+// the conversion; the transposed copy goes through LDS, four rows x four
+// codes at a time.
+constexpr int kPitch = kBlk + 4;  // LDS bytes per row of codes
+template <typename DT, bool VEC>
+__global__ __launch_bounds__(kThreads) void k_quant_weights(QuantWeightsArgs a, int NB, int KB) {
+  __shared__ uint32_t wmax[kThreads / kWave];
+  __shared__ __align__(16) uint8_t tile[kBlk * kPitch];
+  const int tid = threadIdx.x, g = tid / kLanes, l = tid % kLanes;
+  const int kb = blockIdx.x, nb = blockIdx.y, mat = blockIdx.z;
+  const size_t P = (size_t)KB * kBlk, Pt = (size_t)NB * kBlk;
+  const DT *w = static_cast<const DT *>(a.w) + (size_t)mat * a.N * a.K;
+  const int n0 = nb * kBlk, k0 = kb * kBlk;
+  constexpr int kPass = kBlk / kGroups;
+  float f[kPass][8];
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < kPass; ++i) {
+    const int n = n0 + i * kGroups + g;
+    if (n < a.N) {
+      load8<DT, VEC>(w + (size_t)n * a.K, k0 + l * 8, a.K, f[i]);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) f[i][q] = 0.f;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kPass; ++i) m = max(m, amax_bits8(f[i]));
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
+  if (tid % kWave == 0) wmax[tid / kWave] = m;
+  __syncthreads();
+#pragma unroll
+  for (int v = 0; v < kThreads / kWave; ++v) m = max(m, wmax[v]);
+  const int e = scale_exp(m);
+  const float inv = pow2(-e);
+  if (tid == 0) {
+    a.scales[((size_t)mat * NB + nb) * KB + kb] = pow2(e);
+    if (a.scales_t) a.scales_t[((size_t)mat * KB + kb) * NB + nb] = pow2(e);
+  }
+#pragma unroll
+  for (int i = 0; i < kPass; ++i) {
+    const int nl = i * kGroups + g, n = n0 + nl;
+    const uint2 c = make_uint2(codes4(f[i], inv), codes4(f[i] + 4, inv));
+    if (n < a.N) *reinterpret_cast<uint2 *>(a.codes + ((size_t)mat * a.N + n) * P + k0 + l * 8) = c;
+    if (a.codes_t) {
+      uint32_t *t = reinterpret_cast<uint32_t *>(tile + nl * kPitch + l * 8);
+      t[0] = c.x, t[1] = c.y;
+    }
+  }
+  if (!a.codes_t) return;
+  __syncthreads();
+  // 32 lanes write one 128-byte line of a transposed row, 4 rows at a time
+  const int n4 = tid % 32;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int k4 = i * 8 + tid / 32;
+    uint32_t r[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      r[q] = *reinterpret_cast<const uint32_t *>(tile + (n4 * 4 + q) * kPitch + k4 * 4);
+    // bytes q of r[0..3] side by side
+    const uint32_t a01 = __builtin_amdgcn_perm(r[1], r[0], 0x05010400u);  // r0.0 r1.0 r0.1 r1.1
+    const uint32_t a23 = __builtin_amdgcn_perm(r[3], r[2], 0x05010400u);
+    const uint32_t b01 = __builtin_amdgcn_perm(r[1], r[0], 0x07030602u);  // r0.2 r1.2 r0.3 r1.3
+    const uint32_t b23 = __builtin_amdgcn_perm(r[3], r[2], 0x07030602u);
+    const uint32_t o[4] = {
+        __builtin_amdgcn_perm(a23, a01, 0x05040100u), __builtin_amdgcn_perm(a23, a01, 0x07060302u),
+        __builtin_amdgcn_perm(b23, b01, 0x05040100u), __builtin_amdgcn_perm(b23, b01, 0x07060302u)};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int k = k0 + k4 * 4 + q;
+      if (k < a.K)
+        *reinterpret_cast<uint32_t *>(a.codes_t + ((size_t)mat * a.K + k) * Pt + n0 + n4 * 4) = o[q];
+    }
+  }
+}
+
+template <typename DT, bool VEC>
+hipError_t rows_t(const QuantRowsArgs &a, hipStream_t st) {
+  const int KB = (a.K + kBlk - 1) / kBlk;
+  const int groups = (a.M + kGroups - 1) / kGroups;
+  return launch_kernel(k_quant_rows<DT, VEC>, dim3(groups, (KB + kUnroll - 1) / kUnroll), dim3(kThreads),
+                       0, st, a, KB, kUnroll);
+}
+
+template <typename DT, bool VEC>
+hipError_t weights_t(const QuantWeightsArgs &a, hipStream_t st) {
+  const int KB = (a.K + kBlk - 1) / kBlk, NB = (a.N + kBlk - 1) / kBlk;
+  return launch_kernel(k_quant_weights<DT, VEC>, dim3(KB, NB, a.mats), dim3(kThreads), 0, st, a, NB, KB);
+}
+
+}  // namespace
+
+// VEC: rows of a multiple of 16 bytes (and so every chunk of eight elements,
+// or four, inside the row or outside it).
+hipError_t launch_quantize_rows(const QuantRowsArgs &a, bool bf16, hipStream_t st) {
+  if (bf16) return a.K % 8 == 0 ? rows_t<uint16_t, true>(a, st) : rows_t<uint16_t, false>(a, st);
+  return a.K % 4 == 0 ? rows_t<float, true>(a, st) : rows_t<float, false>(a, st);
+}
+
+hipError_t launch_quantize_weights(const QuantWeightsArgs &a, bool bf16, hipStream_t st) {
+  if (bf16) return a.K % 8 == 0 ? weights_t<uint16_t, true>(a, st) : weights_t<uint16_t, false>(a, st);
+  return a.K % 4 == 0 ? weights_t<float, true>(a, st) : weights_t<float, false>(a, st);
+}
+
+}  // namespace moelora

@@ -1,0 +1,434 @@
+// Token order: routed rows sorted by expert, tokens copied into that order,
+// expert outputs added back per token, and the gradients of both.
+//
+// With p = t k + j the routed rows and e(p) their expert (rows with e(p)
+// outside [0, E) dropped), the order is the stable one: pos(p) = #{q : e(q)
+// < e(p)} + #{q < p : e(q) = e(p)}.  Then
+//     dispatch            xs[pos(p)] = x[p / k]
+//     its gradient        dx[t]      = sum_j dxs[pos(t, j)]
+//     combine             out[t]     = sum_j w[t][j] ys[pos(t, j)]
+//     its gradients       dys[pos(p)] = w[p] dout[p / k],
+//                         dw[p]       = <dout[p / k], ys[pos(p)]>
+// All sums run in float32 in ascending j (dw: a fixed tree), each result is
+// rounded once, and nothing uses floating-point atomics, so results repeat
+// bit for bit.  Everything but the order itself is bound by HBM: the copies
+// read each token once and write each routed row once (and the reverse),
+// 16 bytes a lane.
+#include "common.h"
+#include "kernels.h"
+#include "ops.h"
+
+namespace moelora {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / kWave;
+constexpr int kMaxE = 1024;
+// Up to this many routed rows one launch orders and copies: the workgroup of
+// a row finds the row's place by counting (R comparisons), so that a decode
+// step pays one launch.
+constexpr int kFusedRows = 2048;
+
+template <int BYTES> struct Raw;
+template <> struct Raw<16> { typedef u32x4_t type; };
+template <> struct Raw<4> { typedef uint32_t type; };
+template <> struct Raw<2> { typedef uint16_t type; };
+
+__device__ __forceinline__ bool held(int e, int E) { return (unsigned)e < (unsigned)E; }
+
+// One routed row per workgroup (0 .. R-1): its place, then its token's copy.
+// Workgroup R writes expert_start and the sentinel tail of sorted_rows.
+template <int BYTES>
+__global__ __launch_bounds__(kThreads) void k_dispatch_fused(
+    OrderShape s, int chunks, const typename Raw<BYTES>::type *__restrict__ x,
+    const int *__restrict__ ids, int *__restrict__ expert_start, int *__restrict__ sorted_rows,
+    int *__restrict__ row_pos, typename Raw<BYTES>::type *__restrict__ xs) {
+  __shared__ int part[kWaves];
+  __shared__ int hist[kMaxE];
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+  const int R = s.R, E = s.E;
+  if ((int)blockIdx.x < R) {
+    const int p = blockIdx.x;
+    const int e = ids[p];
+    if (!held(e, E)) {  // uniform: the whole workgroup leaves
+      if (tid == 0) row_pos[p] = -1;
+      return;
+    }
+    int n = 0;  // rows before p in the order, this wave's share (uniform)
+    for (int q0 = wave * kWave; q0 < R; q0 += kThreads) {
+      const int q = q0 + lane;
+      const int f = q < R ? ids[q] : -1;
+      n += __popcll(__ballot(held(f, E) && (f < e || (f == e && q < p))));
+    }
+    if (lane == 0) part[wave] = n;
+    __syncthreads();
+    int pos = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) pos += part[w];
+    if (tid == 0) {
+      sorted_rows[pos] = p;
+      row_pos[p] = pos;
+    }
+    if (xs) {
+      const auto *src = x + (size_t)(p / s.k) * chunks;
+      auto *dst = xs + (size_t)pos * chunks;
+      for (int c = tid; c < chunks; c += kThreads) dst[c] = src[c];
+    }
+    return;
+  }
+  for (int e = tid; e < E; e += kThreads) hist[e] = 0;
+  __syncthreads();
+  for (int q = tid; q < R; q += kThreads) {
+    const int f = ids[q];
+    if (held(f, E)) atomicAdd(&hist[f], 1);
+  }
+  __syncthreads();
+  // wave 0: exclusive scan, each lane kMaxE / 64 experts in steps of 64
+  if (wave == 0) {
+    int base = 0;
+    for (int e0 = 0; e0 < E; e0 += kWave) {
+      const int e = e0 + lane;
+      const int n = e < E ? hist[e] : 0;
+      int v = n;
+#pragma unroll
+      for (int d = 1; d < kWave; d <<= 1) {
+        const int u = __shfl_up(v, d);
+        if (lane >= d) v += u;
+      }
+      if (e < E) expert_start[e] = base + v - n;
+      base += __shfl(v, kWave - 1);
+    }
+    if (lane == 0) {
+      expert_start[E] = base;
+      part[0] = base;
+    }
+  }
+  __syncthreads();
+  for (int q = part[0] + tid; q < R; q += kThreads) sorted_rows[q] = R;
+}
+
+// Larger batches, first launch: rows per expert of each chunk of C rows.
+__global__ __launch_bounds__(kThreads) void k_order_count(int R, int E, int C,
+                                                          const int *__restrict__ ids,
+                                                          int *__restrict__ counts) {
+  __shared__ int hist[kMaxE];
+  const int tid = threadIdx.x;
+  for (int e = tid; e < E; e += kThreads) hist[e] = 0;
+  __syncthreads();
+  const int lo = blockIdx.x * C, hi = min(R, lo + C);
+  for (int q = lo + tid; q < hi; q += kThreads) {
+    const int f = ids[q];
+    if (held(f, E)) atomicAdd(&hist[f], 1);
+  }
+  __syncthreads();
+  for (int e = tid; e < E; e += kThreads) counts[(size_t)blockIdx.x * E + e] = hist[e];
+}
+
+// Second launch: places of a chunk's rows.  An expert's first place in the
+// chunk is the experts before it plus the chunks before this one; the waves
+// take a quarter of the chunk each, in order, 64 rows at a time: lanes with
+// the same expert find each other by ballots over the bits of the id, and a
+// lane's rank is the number of equal lanes below it.
+__global__ __launch_bounds__(kThreads) void k_order_place(
+    int R, int E, int C, int nch, int id_bits, const int *__restrict__ ids,
+    const int *__restrict__ counts, int *__restrict__ expert_start, int *__restrict__ sorted_rows,
+    int *__restrict__ row_pos) {
+  __shared__ int next[kWaves][kMaxE];
+  __shared__ int before[kMaxE];
+  __shared__ int wsum[kWaves];
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+  const int me = blockIdx.x;
+  const int lo = me * C, hi = min(R, lo + C);
+  const int quarter = (hi - lo + kWaves - 1) / kWaves;
+  const int wlo = min(hi, lo + wave * quarter), whi = min(hi, wlo + quarter);
+  for (int e = tid; e < kWaves * kMaxE; e += kThreads) (&next[0][0])[e] = 0;
+  __syncthreads();
+  for (int q = wlo + lane; q < whi; q += kWave) {
+    const int f = ids[q];
+    if (held(f, E)) atomicAdd(&next[wave][f], 1);
+  }
+  // totals, and the chunks before this one
+  int kept = 0;
+  for (int e0 = 0; e0 < E; e0 += kThreads) {
+    const int e = e0 + tid;
+    int total = 0, mine = 0;
+    if (e < E) {
+      for (int c = 0; c < nch; ++c) {
+        const int n = counts[(size_t)c * E + e];
+        total += n;
+        mine += c < me ? n : 0;
+      }
+    }
+    int v = total;
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) {
+      const int u = __shfl_up(v, d);
+      if (lane >= d) v += u;
+    }
+    if (lane == kWave - 1) wsum[wave] = v;
+    __syncthreads();
+    int base = kept;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      if (w < wave) base += wsum[w];
+      kept += wsum[w];
+    }
+    if (e < E) {
+      before[e] = base + v - total + mine;
+      if (me == 0) expert_start[e] = base + v - total;
+    }
+    __syncthreads();
+  }
+  if (me == 0 && tid == 0) expert_start[E] = kept;
+  for (int e = tid; e < E; e += kThreads) {
+    int at = before[e];
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const int n = next[w][e];
+      next[w][e] = at;
+      at += n;
+    }
+  }
+  __syncthreads();
+  for (int q0 = wlo; q0 < whi; q0 += kWave) {
+    const int q = q0 + lane;
+    const int f = q < whi ? ids[q] : -1;
+    const bool ok = held(f, E);
+    unsigned long long same = __ballot(ok);
+    for (int b = 0; b < id_bits; ++b) {
+      const unsigned long long on = __ballot(f >> b & 1);
+      same &= (f >> b & 1) ? on : ~on;
+    }
+    if (ok) {
+      const int rank = __popcll(same & ((1ull << lane) - 1));
+      const int at = next[wave][f];  // read by every lane before the first writes it back
+      const int pos = at + rank;
+      sorted_rows[pos] = q;
+      row_pos[q] = pos;
+      if (rank == 0) next[wave][f] = at + __popcll(same);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    } else if (q < whi) {
+      row_pos[q] = -1;
+    }
+  }
+  // the sentinel tail, a share to each workgroup
+  for (int q = kept + me * kThreads + tid; q < R; q += nch * kThreads) sorted_rows[q] = R;
+}
+
+// Threads a token and its tiles: one 16-byte chunk (or less, for rows that
+// are no multiple of 16 bytes) a thread, `tpt` threads side by side.
+struct RowGrid {
+  int tpt_shift, tiles;
+  dim3 grid;
+};
+RowGrid row_grid(int T, int chunks) {
+  int best = 6;  // 64, 128 or 256 threads a token, whichever wastes fewest
+  for (int sh = 7; sh <= 8; ++sh) {
+    const int b = 1 << best, n = 1 << sh;
+    if ((chunks + n - 1) / n * n <= (chunks + b - 1) / b * b) best = sh;
+  }
+  while (best > 0 && (1 << (best - 1)) >= chunks) --best;
+  RowGrid g;
+  g.tpt_shift = best;
+  g.tiles = (chunks + (1 << best) - 1) >> best;
+  const int per = kThreads >> best;
+  g.grid = dim3((T + per - 1) / per, g.tiles);
+  return g;
+}
+
+// xs[pos(t, j)] = x[t] for every j: a token is read once.
+template <int BYTES>
+__global__ __launch_bounds__(kThreads) void k_scatter(
+    OrderShape s, int chunks, int tpt_shift, const typename Raw<BYTES>::type *__restrict__ x,
+    const int *__restrict__ row_pos, typename Raw<BYTES>::type *__restrict__ xs) {
+  const int tpt = 1 << tpt_shift;
+  const int t = blockIdx.x * (kThreads >> tpt_shift) + (threadIdx.x >> tpt_shift);
+  const int c = blockIdx.y * tpt + (threadIdx.x & (tpt - 1));
+  if (t >= s.T || c >= chunks) return;
+  const auto v = x[(size_t)t * chunks + c];
+  const int *pos = row_pos + (size_t)t * s.k;
+  for (int j = 0; j < s.k; ++j) {
+    const int p = pos[j];
+    if ((unsigned)p < (unsigned)s.R) xs[(size_t)p * chunks + c] = v;
+  }
+}
+
+// N elements of a row as float32.
+template <typename DT, int N> struct Pack {
+  DT v[N];
+};
+template <typename DT, int N>
+__device__ __forceinline__ void load_n(const DT *p, float *f) {
+  const Pack<DT, N> a = __builtin_bit_cast(
+      Pack<DT, N>, *reinterpret_cast<const typename Raw<sizeof(DT) * N>::type *>(p));
+#pragma unroll
+  for (int i = 0; i < N; ++i) f[i] = Elem<DT>::to_f32(a.v[i]);
+}
+template <typename DT, int N>
+__device__ __forceinline__ void store_n(DT *p, const float *f) {
+  Pack<DT, N> a;
+#pragma unroll
+  for (int i = 0; i < N; ++i) a.v[i] = Elem<DT>::from_f32(f[i]);
+  *reinterpret_cast<typename Raw<sizeof(DT) * N>::type *>(p) =
+      __builtin_bit_cast(typename Raw<sizeof(DT) * N>::type, a);
+}
+
+// out[t] = sum_j w[t][j] ys[pos(t, j)], ascending j; the loads of four rows
+// are issued together.
+template <typename DT, int N, bool WEIGHTED>
+__global__ __launch_bounds__(kThreads) void k_combine_order(
+    OrderShape s, int chunks, int tpt_shift, const DT *__restrict__ ys,
+    const int *__restrict__ row_pos, const float *__restrict__ w, DT *__restrict__ out) {
+  const int tpt = 1 << tpt_shift;
+  const int t = blockIdx.x * (kThreads >> tpt_shift) + (threadIdx.x >> tpt_shift);
+  const int c = blockIdx.y * tpt + (threadIdx.x & (tpt - 1));
+  if (t >= s.T || c >= chunks) return;
+  float acc[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) acc[i] = 0.f;
+  const int k = s.k;
+  const size_t r0 = (size_t)t * k;
+  constexpr int kBatch = 4;
+  for (int j0 = 0; j0 < k; j0 += kBatch) {
+    float v[kBatch][N], g[kBatch];
+    bool ok[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int p = j0 + b < k ? row_pos[r0 + j0 + b] : -1;
+      ok[b] = (unsigned)p < (unsigned)s.R;
+      g[b] = WEIGHTED && ok[b] ? w[r0 + j0 + b] : 1.f;
+      if (ok[b]) load_n<DT, N>(ys + ((size_t)p * chunks + c) * N, v[b]);
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b)
+      if (ok[b]) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i] = WEIGHTED ? fmaf(g[b], v[b][i], acc[i]) : acc[i] + v[b][i];
+      }
+  }
+  store_n<DT, N>(out + ((size_t)t * chunks + c) * N, acc);
+}
+
+// One wave per routed row: dys[pos] = w dout[t], dw = <dout[t], ys[pos]>.
+template <typename DT, int N>
+__global__ __launch_bounds__(kThreads) void k_combine_backward(
+    OrderShape s, int chunks, const DT *__restrict__ dout, const DT *__restrict__ ys,
+    const int *__restrict__ row_pos, const float *__restrict__ w, DT *__restrict__ dys,
+    float *__restrict__ dw) {
+  const int lane = threadIdx.x & (kWave - 1);
+  const int p = __builtin_amdgcn_readfirstlane(blockIdx.x * kWaves + threadIdx.x / kWave);
+  if (p >= s.R) return;
+  const int pos = row_pos[p];
+  if ((unsigned)pos >= (unsigned)s.R) {
+    if (dw && lane == 0) dw[p] = 0.f;
+    return;
+  }
+  const float g = w ? w[p] : 1.f;
+  const DT *d = dout + (size_t)(p / s.k) * chunks * N;
+  const size_t row = (size_t)pos * chunks * N;
+  float sum = 0.f;
+#pragma unroll 2
+  for (int c = lane; c < chunks; c += kWave) {
+    float a[N], o[N];
+    load_n<DT, N>(d + (size_t)c * N, a);
+    if (dw) {
+      float y[N];
+      load_n<DT, N>(ys + row + (size_t)c * N, y);
+#pragma unroll
+      for (int i = 0; i < N; ++i) sum = fmaf(a[i], y[i], sum);
+    }
+    if (dys) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) o[i] = g * a[i];
+      store_n<DT, N>(dys + row + (size_t)c * N, o);
+    }
+  }
+  if (dw) {
+#pragma unroll
+    for (int m = kWave / 2; m > 0; m >>= 1) sum += __shfl_xor(sum, m);
+    if (lane == 0) dw[p] = sum;
+  }
+}
+
+template <int BYTES>
+hipError_t dispatch_t(const OrderShape &s, size_t row_bytes, const void *x, const int *ids,
+                      int *expert_start, int *sorted_rows, int *row_pos, void *xs, int *counts,
+                      hipStream_t st) {
+  typedef typename Raw<BYTES>::type V;
+  const int chunks = (int)(row_bytes / BYTES);
+  const V *vx = static_cast<const V *>(x);
+  V *vxs = static_cast<V *>(xs);
+  if (s.R <= kFusedRows)
+    return launch_kernel(k_dispatch_fused<BYTES>, dim3(s.R + 1), dim3(kThreads), 0, st, s, chunks, vx,
+                         ids, expert_start, sorted_rows, row_pos, vxs);
+  const int C = order_chunk_rows(s.R), nch = order_chunks(s.R);
+  int bits = 0;
+  while ((1 << bits) < s.E) ++bits;
+  hipError_t e = launch_kernel(k_order_count, dim3(nch), dim3(kThreads), 0, st, s.R, s.E, C, ids, counts);
+  if (e != hipSuccess) return e;
+  e = launch_kernel(k_order_place, dim3(nch), dim3(kThreads), 0, st, s.R, s.E, C, nch, bits, ids,
+                    static_cast<const int *>(counts), expert_start, sorted_rows, row_pos);
+  if (e != hipSuccess || !xs) return e;
+  const RowGrid g = row_grid(s.T, chunks);
+  return launch_kernel(k_scatter<BYTES>, g.grid, dim3(kThreads), 0, st, s, chunks, g.tpt_shift, vx,
+                       static_cast<const int *>(row_pos), vxs);
+}
+
+template <typename DT, int N>
+hipError_t combine_t(const OrderShape &s, const void *ys, const int *row_pos, const float *w, void *out,
+                     hipStream_t st) {
+  const int chunks = s.H / N;
+  const RowGrid g = row_grid(s.T, chunks);
+  if (w)
+    return launch_kernel(k_combine_order<DT, N, true>, g.grid, dim3(kThreads), 0, st, s, chunks,
+                         g.tpt_shift, static_cast<const DT *>(ys), row_pos, w, static_cast<DT *>(out));
+  return launch_kernel(k_combine_order<DT, N, false>, g.grid, dim3(kThreads), 0, st, s, chunks,
+                       g.tpt_shift, static_cast<const DT *>(ys), row_pos, w, static_cast<DT *>(out));
+}
+
+template <typename DT, int N>
+hipError_t combine_backward_t(const OrderShape &s, const void *dout, const void *ys, const int *row_pos,
+                              const float *w, void *dys, float *dw, hipStream_t st) {
+  return launch_kernel(k_combine_backward<DT, N>, dim3((s.R + kWaves - 1) / kWaves), dim3(kThreads), 0,
+                       st, s, s.H / N, static_cast<const DT *>(dout), static_cast<const DT *>(ys),
+                       row_pos, w, static_cast<DT *>(dys), dw);
+}
+
+}  // namespace
+
+int dispatch_counts(int R) { return R <= kFusedRows ? 0 : order_chunks(R); }
+
+// Rows of a multiple of 16 bytes move 16 bytes a lane, others 4 or 2.
+hipError_t launch_dispatch(const OrderShape &s, const void *x, const int *ids, int *expert_start,
+                           int *sorted_rows, int *row_pos, void *xs, int *counts, hipStream_t st) {
+  const size_t b = (size_t)s.H * (s.bf16 ? 2 : 4);
+  if (b % 16 == 0) return dispatch_t<16>(s, b, x, ids, expert_start, sorted_rows, row_pos, xs, counts, st);
+  if (b % 4 == 0) return dispatch_t<4>(s, b, x, ids, expert_start, sorted_rows, row_pos, xs, counts, st);
+  return dispatch_t<2>(s, b, x, ids, expert_start, sorted_rows, row_pos, xs, counts, st);
+}
+
+hipError_t launch_combine_rows(const OrderShape &s, const void *ys, const int *row_pos, const float *w,
+                               void *out, hipStream_t st) {
+  if (s.bf16) {
+    if (s.H % 8 == 0) return combine_t<uint16_t, 8>(s, ys, row_pos, w, out, st);
+    if (s.H % 2 == 0) return combine_t<uint16_t, 2>(s, ys, row_pos, w, out, st);
+    return combine_t<uint16_t, 1>(s, ys, row_pos, w, out, st);
+  }
+  if (s.H % 4 == 0) return combine_t<float, 4>(s, ys, row_pos, w, out, st);
+  return combine_t<float, 1>(s, ys, row_pos, w, out, st);
+}
+
+hipError_t launch_combine_backward(const OrderShape &s, const void *dout, const void *ys,
+                                   const int *row_pos, const float *w, void *dys, float *dw,
+                                   hipStream_t st) {
+  if (s.bf16) {
+    if (s.H % 8 == 0) return combine_backward_t<uint16_t, 8>(s, dout, ys, row_pos, w, dys, dw, st);
+    if (s.H % 2 == 0) return combine_backward_t<uint16_t, 2>(s, dout, ys, row_pos, w, dys, dw, st);
+    return combine_backward_t<uint16_t, 1>(s, dout, ys, row_pos, w, dys, dw, st);
+  }
+  if (s.H % 4 == 0) return combine_backward_t<float, 4>(s, dout, ys, row_pos, w, dys, dw, st);
+  return combine_backward_t<float, 1>(s, dout, ys, row_pos, w, dys, dw, st);
+}
+
+}  // namespace moelora
