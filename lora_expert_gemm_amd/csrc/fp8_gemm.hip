@@ -227,19 +227,22 @@ __global__ __launch_bounds__(kSThreads) void k_fp8_stream(Fp8GemmArgs a) {
 
 // --------------------------------------------------------------- many rows
 //
-// 16 TT rows x 512 weight rows (SILU: 256 gate + the matching 256 up) a
-// workgroup, 8 waves, one workgroup per CU.  A slab is one block of 128: a
-// row contributes one 128-byte line, fetched by 8 lanes straight into LDS;
-// two LDS stages of 80 KB, the loads of slab b + 1 in flight while the MFMAs
-// of slab b run; one barrier a slab.  A row's 16-byte chunk c sits at chunk
-// c ^ ((row / 2) % 8) of its LDS row, so the 16 rows that 16 lanes read at
-// one chunk fall on 16 distinct bank groups.  Each wave holds 64 weight rows
-// x 128 tokens (128 accumulator registers): 24 KB of LDS reads for 32 MFMAs
-// a slab, 0.75 of the LDS rate the MFMAs leave.  Rows past the expert's
-// last, and weight rows past N, lie past their buffer resource's end: their
-// loads fetch nothing, and their outputs are dropped.
-constexpr int kGW = 512;
-constexpr int kGWaves = 8, kGThreads = kGWaves * kWave;
+// 16 TT rows x 256 weight rows (SILU: 128 gate + the matching 128 up) a
+// workgroup of 4 waves, two workgroups per CU.  A wave owns 64 weight rows
+// and all 16 TT tokens, so no other wave reads its weights: they go straight
+// into its registers, one slab (a block of 128) ahead, and LDS holds only
+// what the waves share, the token rows and their scales, two slabs ahead in
+// three stages.  (Weights through LDS too, 128 x 512 tiles of 8 waves: 672 us
+// for the 25600-row gate_up product, of which ~190 us were the extra LDS
+// fills and 140 us the fragment reads.)  A token row contributes one 128-byte
+// line a slab, fetched by 8 lanes; its 16-byte chunk c sits at chunk
+// c ^ ((row / 2) % 8) of the LDS row, so the 16 rows that 16 lanes read at
+// one chunk fall on 16 distinct bank groups.  Rows past the expert's last,
+// and weight rows past N, lie past their buffer resource's end: their loads
+// fetch nothing, and their outputs are dropped.
+constexpr int kGWaves = 4, kGThreads = kGWaves * kWave;
+constexpr int kGW = 64 * kGWaves;
+constexpr int kGSlots = 3;
 
 __device__ __forceinline__ int lds_off(int row, int c) {
   return row * 128 + ((c ^ ((row >> 1) & 7)) << 4);
@@ -296,10 +299,12 @@ __device__ __forceinline__ RowTile find_tile(const Fp8GemmArgs &a, int BM, int n
 }
 
 template <int TT, bool SILU, typename OT>
-__global__ __launch_bounds__(kGThreads, 1) void k_fp8_tiled(Fp8GemmArgs a, int ncols) {
+__global__ __launch_bounds__(kGThreads, 2) void k_fp8_tiled(Fp8GemmArgs a, int ncols) {
   extern __shared__ __align__(16) unsigned char smem[];
-  constexpr int HV = SILU ? 2 : 1, COLS = kGW / HV;
-  constexpr int GM = 16 * TT, STAGE = (GM + kGW) * 128, XL = TT / 4;
+  constexpr int HV = SILU ? 2 : 1, COLS = kGW / HV, WC = 64 / HV;  // columns a workgroup, a wave
+  constexpr int GM = 16 * TT, STAGE = GM * 128 + 512;
+  constexpr int XL = GM / 8 / kGWaves;  // token loads a wave and slab
+  constexpr int kAfter = 8 + XL + 1;    // vector loads issued after a slab's tokens, see step()
   typedef Block<sizeof(OT) == 4> B;
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -308,97 +313,122 @@ __global__ __launch_bounds__(kGThreads, 1) void k_fp8_tiled(Fp8GemmArgs a, int n
   if (rt.e < 0) return;
   const int n0 = rt.nt * COLS, rows = min(GM, rt.hi - rt.m0), cols = min(COLS, a.N - n0);
   const size_t P = a.P;
+  const int KB = a.KB;
 
-  // load plan: weight groups of 8 rows 8 wave .. + 7, token groups XL wave ..
-  const int half = SILU ? wave / (kGWaves / 2) : 0;
-  const __amdgpu_buffer_rsrc_t wres = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<uint8_t *>(a.w) + (((size_t)rt.e * HV + half) * a.N + n0) * P, (short)0,
-      (int)(cols * P), kBufferWord3);
-  const __amdgpu_buffer_rsrc_t xres = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<uint8_t *>(a.x) + (size_t)rt.m0 * P, (short)0, (int)(rows * P), kBufferWord3);
-  uint32_t voff[10];  // (a dependent type here would have the host pass check the builtins below)
+  // Buffer resources of the tile; slabs past the last get an empty one, so
+  // the loop issues its loads unconditionally and they fetch nothing.
+  const size_t mat = (size_t)rt.e * HV;
+  const uint8_t *wbase[2] = {a.w + (mat * a.N + n0) * P, a.w + ((mat + HV - 1) * a.N + n0) * P};
+  auto resource = [&](const void *base, int bytes, int b) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, b < KB ? bytes : 0,
+                                             kBufferWord3);
+  };
+  uint32_t woff[4];  // the lane's row of the wave's four weight tiles (SILU: 2 gate, 2 up)
 #pragma unroll
-  for (int j = 0; j < 8 + XL; ++j) {
-    const int r = j < 8 ? 64 * wave + 8 * j + (lane >> 3)
-                        : kGW + 8 * XL * wave + 8 * (j - 8) + (lane >> 3);
-    const int c = (lane & 7) ^ ((r >> 1) & 7);
-    const int local = j < 8 ? r - half * COLS : r - kGW;
-    voff[j] = (uint32_t)(local * P) + 16 * c;
+  for (int i = 0; i < 4; ++i)
+    woff[i] = (uint32_t)((WC * wave + 16 * (SILU ? i % 2 : i) + l16) * P) + 16 * g;
+  uint32_t xoff[4];
+#pragma unroll
+  for (int j = 0; j < XL; ++j) {
+    const int r = 8 * (XL * wave + j) + (lane >> 3);
+    xoff[j] = (uint32_t)(r * P) + 16 * ((lane & 7) ^ ((r >> 1) & 7));
   }
-  auto issue = [&](int b, int buf) {
-    unsigned char *st = smem + buf * STAGE;
+  struct Weights {
+    typename Block<false>::Operand v[4];
+  };
+  auto load_w = [&](Weights &w, int b) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          wres, (__attribute__((address_space(3))) void *)(st + (64 * wave + 8 * j) * 128), 16, voff[j],
-          b * 128, 0, 0);
+    for (int i = 0; i < 4; ++i) {
+      const __amdgpu_buffer_rsrc_t res = resource(wbase[SILU ? i / 2 : 0], (int)(cols * P), b);
+      w.v[i] = {__builtin_amdgcn_raw_buffer_load_b128(res, woff[i], b * 128, 0),
+                __builtin_amdgcn_raw_buffer_load_b128(res, woff[i] + 64, b * 128, 0)};
+    }
+  };
+  // tokens and their scales (64 a wave, twice over) of slab b
+  auto issue_x = [&](int b) {
+    unsigned char *st = smem + b % kGSlots * STAGE;
+    const __amdgpu_buffer_rsrc_t xres = resource(a.x + (size_t)rt.m0 * P, (int)(rows * P), b);
 #pragma unroll
     for (int j = 0; j < XL; ++j)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          xres, (__attribute__((address_space(3))) void *)(st + (kGW + 8 * XL * wave + 8 * j) * 128), 16,
-          voff[8 + j], b * 128, 0, 0);
+          xres, (__attribute__((address_space(3))) void *)(st + 8 * (XL * wave + j) * 128), 16, xoff[j],
+          b * 128, 0, 0);
+    const __amdgpu_buffer_rsrc_t sres = resource(a.xs + (size_t)b * a.R + rt.m0, rows * 4, b);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        sres, (__attribute__((address_space(3))) void *)(st + GM * 128 + 256 * (wave & 1)), 4,
+        256 * (wave & 1) + 4 * lane, 0, 0, 0);
   };
-
-  // scales of a slab: this lane's token in each of the eight groups, and the
-  // wave's weight block of each half (64, or 32 + 32, weight rows lie in one)
-  const int wcol = SILU ? 32 * wave : 64 * wave;
-  const float *wsp = a.ws + ((size_t)rt.e * HV * a.NB + min((n0 + wcol) / 128, a.NB - 1)) * a.KB;
-  struct Scales {
-    float x[TT], w[HV];
-  };
-  auto scales = [&](Scales &s, int b) {
-    const __amdgpu_buffer_rsrc_t sres = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<float *>(a.xs) + (size_t)b * a.R + rt.m0, (short)0, rows * 4, kBufferWord3);
-#pragma unroll
-    for (int t = 0; t < TT; ++t)
-      s.x[t] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(sres, l16 * 4, 64 * t, 0));
-#pragma unroll
-    for (int h = 0; h < HV; ++h) s.w[h] = wsp[(size_t)h * a.NB * a.KB + b];
-  };
+  // scales of the wave's weight block: 64 slabs at a time, one a lane (the
+  // wave's 64, or 32 + 32, weight rows lie in one block of 128)
+  const float *wsp = a.ws + (mat * a.NB + min((n0 + WC * wave) / 128, a.NB - 1)) * KB;
+  float ws[HV];
 
   f32x4_t acc[4][TT];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int t = 0; t < TT; ++t) acc[i][t] = f32x4_t{0, 0, 0, 0};
-  int wrow[4];  // LDS rows of the wave's four weight tiles
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    wrow[i] = (SILU ? (i / 2) * COLS + 32 * wave + 16 * (i % 2) : 64 * wave + 16 * i) + l16;
 
-  Scales cur, nxt;
-  issue(0, 0);
-  scales(nxt, 0);
-  for (int b = 0; b < a.KB; ++b) {
-    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): this wave's loads of slab b have landed
-    __syncthreads();                     // ... and every wave's; slab b - 1 is read out
-    cur = nxt;
-    if (b + 1 < a.KB) {
-      issue(b + 1, (b + 1) & 1);
-      scales(nxt, b + 1);
-    }
-    const unsigned char *st = smem + (b & 1) * STAGE;
-    typename B::Operand w[4];
+  // Slab b with its weights in `w`; loads slab b + 1's into `wn`.  The wait
+  // at the top is for slab b's tokens: issued at slab b - 2, and after them
+  // the weights of b and the tokens of b + 1 at slab b - 1, kAfter loads
+  // that may still be in flight (nothing moves across the barrier).
+  auto step = [&](int b, const Weights &w, Weights &wn) {
+    __builtin_amdgcn_s_waitcnt(0x0f70 | kAfter);
+    __builtin_amdgcn_s_barrier();
+    if (b % kWave == 0) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      w[i] = B::load(*reinterpret_cast<const u32x4_t *>(st + lds_off(wrow[i], g)),
-                     *reinterpret_cast<const u32x4_t *>(st + lds_off(wrow[i], g + 4)));
+      for (int h = 0; h < HV; ++h) ws[h] = wsp[(size_t)h * a.NB * KB + min(b + lane, KB - 1)];
+    }
+    load_w(wn, b + 1);
+    issue_x(b + 2);
+    const unsigned char *st = smem + b % kGSlots * STAGE;
+    const float *sx = reinterpret_cast<const float *>(st + GM * 128);
+    float sw[HV];
+#pragma unroll
+    for (int h = 0; h < HV; ++h)
+      sw[h] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ws[h]), b % kWave));
+    typename B::Operand wo[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) wo[i] = B::load(w.v[i].lo, w.v[i].hi);
+    // token fragments one group ahead of their MFMAs; the scheduling barrier
+    // keeps the compiler from reading all groups at once (registers)
+    auto read_x = [&](int t, u32x4_t &lo, u32x4_t &hi) {
+      const int r = 16 * t + l16;
+      lo = *reinterpret_cast<const u32x4_t *>(st + lds_off(r, g));
+      hi = *reinterpret_cast<const u32x4_t *>(st + lds_off(r, g + 4));
+    };
+    u32x4_t xlo[2], xhi[2];
+    read_x(0, xlo[0], xhi[0]);
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
-      const int r = kGW + 16 * t + l16;
-      const typename B::Operand x = B::load(*reinterpret_cast<const u32x4_t *>(st + lds_off(r, g)),
-                                            *reinterpret_cast<const u32x4_t *>(st + lds_off(r, g + 4)));
+      if (t + 1 < TT) read_x(t + 1, xlo[(t + 1) & 1], xhi[(t + 1) & 1]);
+      const float sxt = sx[16 * t + l16];
+      const typename B::Operand x = B::load(xlo[t & 1], xhi[t & 1]);
       f32x4_t p[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) p[i] = B::mma(w[i], x);
+      for (int i = 0; i < 4; ++i) p[i] = B::mma(wo[i], x);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float s = cur.x[t] * cur.w[SILU ? i / 2 : 0];
+        const float s = sxt * sw[SILU ? i / 2 : 0];
 #pragma unroll
         for (int v = 0; v < 4; ++v) acc[i][t][v] = fmaf(s, p[i][v], acc[i][t][v]);
       }
+      __builtin_amdgcn_sched_barrier(0);
     }
+  };
+
+  Weights wa, wb;
+  issue_x(0);
+  load_w(wa, 0);
+  issue_x(1);
+  int b = 0;
+  for (; b + 1 < KB; b += 2) {
+    step(b, wa, wb);
+    step(b + 1, wb, wa);
   }
+  if (b < KB) step(b, wa, wb);
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // no load of this workgroup outlives it
 
 #pragma unroll
   for (int t = 0; t < TT; ++t) {
@@ -407,7 +437,7 @@ __global__ __launch_bounds__(kGThreads, 1) void k_fp8_tiled(Fp8GemmArgs a, int n
     OT *row = static_cast<OT *>(a.out) + (size_t)(rt.m0 + m) * a.N;
 #pragma unroll
     for (int i = 0; i < (SILU ? 2 : 4); ++i) {
-      const int n = n0 + wcol + 16 * i + 4 * g;
+      const int n = n0 + WC * wave + 16 * i + 4 * g;
       if (n >= a.N) continue;
       float o[4];
 #pragma unroll
@@ -426,7 +456,7 @@ hipError_t stream_t(const Fp8GemmArgs &a, hipStream_t st) {
 
 template <int TT, bool SILU, typename OT>
 hipError_t tiled_t(const Fp8GemmArgs &a, hipStream_t st) {
-  constexpr int COLS = kGW / (SILU ? 2 : 1), GM = 16 * TT, LDS = 2 * (GM + kGW) * 128;
+  constexpr int COLS = kGW / (SILU ? 2 : 1), GM = 16 * TT, LDS = kGSlots * (GM * 128 + 512);
   auto kern = k_fp8_tiled<TT, SILU, OT>;
   hipError_t err = hipFuncSetAttribute(reinterpret_cast<const void *>(kern),
                                        hipFuncAttributeMaxDynamicSharedMemorySize, LDS);
