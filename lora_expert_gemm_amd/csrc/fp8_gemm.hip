@@ -242,7 +242,8 @@ __global__ __launch_bounds__(kSThreads) void k_fp8_stream(Fp8GemmArgs a) {
 // fetch nothing, and their outputs are dropped.
 constexpr int kGWaves = 4, kGThreads = kGWaves * kWave;
 constexpr int kGW = 64 * kGWaves;
-constexpr int kGSlots = 3;
+constexpr int kGSlots = 2;              // stages of tokens
+constexpr int kGWaveW = 64 * 128;        // LDS bytes of a wave's weights
 
 __device__ __forceinline__ int lds_off(int row, int c) {
   return row * 128 + ((c ^ ((row >> 1) & 7)) << 4);
@@ -304,7 +305,6 @@ __global__ __launch_bounds__(kGThreads, 2) void k_fp8_tiled(Fp8GemmArgs a, int n
   constexpr int HV = SILU ? 2 : 1, COLS = kGW / HV, WC = 64 / HV;  // columns a workgroup, a wave
   constexpr int GM = 16 * TT, STAGE = GM * 128 + 512;
   constexpr int XL = GM / 8 / kGWaves;  // token loads a wave and slab
-  constexpr int kAfter = 8 + XL + 1;    // vector loads issued after a slab's tokens, see step()
   typedef Block<sizeof(OT) == 4> B;
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -323,26 +323,39 @@ __global__ __launch_bounds__(kGThreads, 2) void k_fp8_tiled(Fp8GemmArgs a, int n
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, b < KB ? bytes : 0,
                                              kBufferWord3);
   };
-  uint32_t woff[4];  // the lane's row of the wave's four weight tiles (SILU: 2 gate, 2 up)
+  // load plans: a wave instruction fills 8 LDS rows (1 KB), lane i bringing
+  // the chunk that lds_off places at byte 16 i of the group.  The wave's 64
+  // weight rows are WC of each half.
+  uint32_t woff[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    woff[i] = (uint32_t)((WC * wave + 16 * (SILU ? i % 2 : i) + l16) * P) + 16 * g;
+  for (int j = 0; j < WC / 8; ++j) {
+    const int r = 8 * j + (lane >> 3);
+    woff[j] = (uint32_t)((WC * wave + r) * P) + 16 * ((lane & 7) ^ ((r >> 1) & 7));
+  }
   uint32_t xoff[4];
 #pragma unroll
   for (int j = 0; j < XL; ++j) {
     const int r = 8 * (XL * wave + j) + (lane >> 3);
     xoff[j] = (uint32_t)(r * P) + 16 * ((lane & 7) ^ ((r >> 1) & 7));
   }
+  unsigned char *const wst = smem + kGSlots * STAGE + wave * kGWaveW;
   struct Weights {
     typename Block<false>::Operand v[4];
   };
-  auto load_w = [&](Weights &w, int b) {
+  auto issue_w = [&](int b) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __amdgpu_buffer_rsrc_t res = resource(wbase[SILU ? i / 2 : 0], (int)(cols * P), b);
-      w.v[i] = {__builtin_amdgcn_raw_buffer_load_b128(res, woff[i], b * 128, 0),
-                __builtin_amdgcn_raw_buffer_load_b128(res, woff[i] + 64, b * 128, 0)};
+    for (int j = 0; j < 8; ++j) {
+      const __amdgpu_buffer_rsrc_t res = resource(wbase[j * 8 / WC], (int)(cols * P), b);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          res, (__attribute__((address_space(3))) void *)(wst + 8 * j * 128), 16, woff[j % (WC / 8)],
+          b * 128, 0, 0);
     }
+  };
+  auto read_w = [&](Weights &w) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w.v[i] = {*reinterpret_cast<const u32x4_t *>(wst + lds_off(16 * i + l16, g)),
+                *reinterpret_cast<const u32x4_t *>(wst + lds_off(16 * i + l16, g + 4))};
   };
   // tokens and their scales (64 a wave, twice over) of slab b
   auto issue_x = [&](int b) {
@@ -369,19 +382,18 @@ __global__ __launch_bounds__(kGThreads, 2) void k_fp8_tiled(Fp8GemmArgs a, int n
 #pragma unroll
     for (int t = 0; t < TT; ++t) acc[i][t] = f32x4_t{0, 0, 0, 0};
 
-  // Slab b with its weights in `w`; loads slab b + 1's into `wn`.  The wait
-  // at the top is for slab b's tokens: issued at slab b - 2, and after them
-  // the weights of b and the tokens of b + 1 at slab b - 1, kAfter loads
-  // that may still be in flight (nothing moves across the barrier).
+  // Slab b with its weights in `w`; reads slab b + 1's into `wn` half way.
+  // The waits count this wave's own loads in their order of issue: tokens of
+  // b + 1 (XL + 1 loads, top of slab b), weights of b + 2 (8 loads, middle of
+  // slab b); nothing moves across the barrier or the waits.
   auto step = [&](int b, const Weights &w, Weights &wn) {
-    __builtin_amdgcn_s_waitcnt(0x0f70 | kAfter);
-    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_s_waitcnt(0x0f70 | 8);  // tokens of b landed; weights of b + 1 may not have
+    __builtin_amdgcn_s_barrier();            // ... for every wave, and slab b - 1 is read out
     if (b % kWave == 0) {
 #pragma unroll
       for (int h = 0; h < HV; ++h) ws[h] = wsp[(size_t)h * a.NB * KB + min(b + lane, KB - 1)];
     }
-    load_w(wn, b + 1);
-    issue_x(b + 2);
+    issue_x(b + 1);
     const unsigned char *st = smem + b % kGSlots * STAGE;
     const float *sx = reinterpret_cast<const float *>(st + GM * 128);
     float sw[HV];
@@ -415,13 +427,24 @@ __global__ __launch_bounds__(kGThreads, 2) void k_fp8_tiled(Fp8GemmArgs a, int n
         for (int v = 0; v < 4; ++v) acc[i][t][v] = fmaf(s, p[i][v], acc[i][t][v]);
       }
       __builtin_amdgcn_sched_barrier(0);
+      if (t == TT / 2 - 1) {
+        __builtin_amdgcn_s_waitcnt(0x0f70 | (XL + 1));  // weights of b + 1 landed
+        read_w(wn);
+      }
+      if (t == TT / 2) {
+        __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): read out, their place is free
+        issue_w(b + 2);
+      }
     }
   };
 
   Weights wa, wb;
+  issue_w(0);
+  __builtin_amdgcn_s_waitcnt(0x0f70);
+  read_w(wa);
+  __builtin_amdgcn_s_waitcnt(0xc07f);
   issue_x(0);
-  load_w(wa, 0);
-  issue_x(1);
+  issue_w(1);
   int b = 0;
   for (; b + 1 < KB; b += 2) {
     step(b, wa, wb);
@@ -456,7 +479,7 @@ hipError_t stream_t(const Fp8GemmArgs &a, hipStream_t st) {
 
 template <int TT, bool SILU, typename OT>
 hipError_t tiled_t(const Fp8GemmArgs &a, hipStream_t st) {
-  constexpr int COLS = kGW / (SILU ? 2 : 1), GM = 16 * TT, LDS = kGSlots * (GM * 128 + 512);
+  constexpr int COLS = kGW / (SILU ? 2 : 1), GM = 16 * TT, LDS = kGSlots * (GM * 128 + 512) + kGWaves * kGWaveW;
   auto kern = k_fp8_tiled<TT, SILU, OT>;
   hipError_t err = hipFuncSetAttribute(reinterpret_cast<const void *>(kern),
                                        hipFuncAttributeMaxDynamicSharedMemorySize, LDS);
