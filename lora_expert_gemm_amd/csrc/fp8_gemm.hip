@@ -382,6 +382,18 @@ __global__ __launch_bounds__(kGThreads, 2) void k_fp8_tiled(Fp8GemmArgs a, int n
 #pragma unroll
     for (int t = 0; t < TT; ++t) acc[i][t] = f32x4_t{0, 0, 0, 0};
 
+  // block sums not yet added, and their scales
+  f32x4_t p[4];
+  float s[HV];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) p[i] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+  for (int h = 0; h < HV; ++h) s[h] = 0.f;
+  auto add = [&](int i, int t) {
+#pragma unroll
+    for (int v = 0; v < 4; ++v) acc[i][t][v] = fmaf(s[SILU ? i / 2 : 0], p[i][v], acc[i][t][v]);
+  };
+
   // Slab b with its weights in `w`; reads slab b + 1's into `wn` half way.
   // The waits count this wave's own loads in their order of issue: tokens of
   // b + 1 (XL + 1 loads, top of slab b), weights of b + 2 (8 loads, middle of
@@ -417,15 +429,16 @@ __global__ __launch_bounds__(kGThreads, 2) void k_fp8_tiled(Fp8GemmArgs a, int n
       if (t + 1 < TT) read_x(t + 1, xlo[(t + 1) & 1], xhi[(t + 1) & 1]);
       const float sxt = sx[16 * t + l16];
       const typename B::Operand x = B::load(xlo[t & 1], xhi[t & 1]);
-      f32x4_t p[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) p[i] = B::mma(wo[i], x);
+      // a block sum is scaled and added just before its register takes the
+      // next group's: four MFMAs later, so nothing waits for the matrix core
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float s = sxt * sw[SILU ? i / 2 : 0];
-#pragma unroll
-        for (int v = 0; v < 4; ++v) acc[i][t][v] = fmaf(s, p[i][v], acc[i][t][v]);
+        add(i, t == 0 ? TT - 1 : t - 1);
+        p[i] = B::mma(wo[i], x);
+        __builtin_amdgcn_sched_barrier(0);
       }
+#pragma unroll
+      for (int h = 0; h < HV; ++h) s[h] = sxt * sw[h];
       __builtin_amdgcn_sched_barrier(0);
       if (t == TT / 2 - 1) {
         __builtin_amdgcn_s_waitcnt(0x0f70 | (XL + 1));  // weights of b + 1 landed
@@ -451,6 +464,8 @@ __global__ __launch_bounds__(kGThreads, 2) void k_fp8_tiled(Fp8GemmArgs a, int n
     step(b + 1, wb, wa);
   }
   if (b < KB) step(b, wa, wb);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) add(i, TT - 1);
   __builtin_amdgcn_s_waitcnt(0x0f70);  // no load of this workgroup outlives it
 
 #pragma unroll
