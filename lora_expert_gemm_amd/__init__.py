@@ -233,17 +233,25 @@ def moelora_timing_end(plan):
 # is passed on: contiguous, on the current device, elements of the expected
 # size and at least as many as the call reads or writes.
 
-def _buf(t, n, size, name, optional=False):
+def _where(stream):
+    """The stream to enqueue on (None: the current one) and the current device."""
+    if stream is None:
+        s = torch.cuda.current_stream()
+        return s.cuda_stream, s.device_index
+    return _stream(stream), torch.cuda.current_device() if torch.cuda.is_available() else -1
+
+
+def _buf(t, n, size, dev, name, optional=False):
     if t is None:
         if optional or n == 0:
             return None
         raise ValueError(f"{name} is required")
     if isinstance(t, int):
         return t
-    if t.numel() < n or t.element_size() != size or not t.is_contiguous():
+    if t.numel() < n or t.itemsize != size or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous tensor of at least {n} elements of "
                          f"{size} bytes, got {tuple(t.shape)} {t.dtype} strides {t.stride()}")
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+    if t.get_device() != dev or dev < 0:
         raise ValueError(f"{name} is on {t.device}, not on the current device")
     return t.data_ptr()
 
@@ -262,75 +270,82 @@ def moelora_dispatch_workspace(n_tokens, n_experts, top_k):
 
 def moelora_dispatch(n_tokens, hidden, n_experts, top_k, dtype, x, topk_ids, expert_start,
                      sorted_rows, row_pos, xs, workspace, workspace_bytes, stream=None):
+    st, dev = _where(stream)
     R, es = n_tokens * top_k, _es(dtype)
     _check(_lib.moelora_dispatch(
         n_tokens, hidden, n_experts, top_k, dtype,
-        _buf(x, n_tokens * hidden, es, "x", xs is None), _buf(topk_ids, R, 4, "topk_ids"),
-        _buf(expert_start, n_experts + 1, 4, "expert_start"),
-        _buf(sorted_rows, R, 4, "sorted_rows"), _buf(row_pos, R, 4, "row_pos"),
-        _buf(xs, R * hidden, es, "xs", True),
-        _buf(workspace, workspace_bytes, 1, "workspace", True), workspace_bytes,
-        _stream(stream)), "moelora_dispatch")
+        _buf(x, n_tokens * hidden, es, dev, "x", xs is None), _buf(topk_ids, R, 4, dev, "topk_ids"),
+        _buf(expert_start, n_experts + 1, 4, dev, "expert_start"),
+        _buf(sorted_rows, R, 4, dev, "sorted_rows"), _buf(row_pos, R, 4, dev, "row_pos"),
+        _buf(xs, R * hidden, es, dev, "xs", True),
+        _buf(workspace, workspace_bytes, 1, dev, "workspace", True), workspace_bytes,
+        st), "moelora_dispatch")
 
 
 def moelora_dispatch_backward(n_tokens, hidden, top_k, dtype, dxs, row_pos, dx, stream=None):
+    st, dev = _where(stream)
     R, es = n_tokens * top_k, _es(dtype)
     _check(_lib.moelora_dispatch_backward(
-        n_tokens, hidden, top_k, dtype, _buf(dxs, R * hidden, es, "dxs"),
-        _buf(row_pos, R, 4, "row_pos"), _buf(dx, n_tokens * hidden, es, "dx"), _stream(stream)),
+        n_tokens, hidden, top_k, dtype, _buf(dxs, R * hidden, es, dev, "dxs"),
+        _buf(row_pos, R, 4, dev, "row_pos"), _buf(dx, n_tokens * hidden, es, dev, "dx"), st),
         "moelora_dispatch_backward")
 
 
 def moelora_combine(n_tokens, hidden, top_k, dtype, ys, row_pos, topk_w, out, stream=None):
+    st, dev = _where(stream)
     R, es = n_tokens * top_k, _es(dtype)
     _check(_lib.moelora_combine(
-        n_tokens, hidden, top_k, dtype, _buf(ys, R * hidden, es, "ys"),
-        _buf(row_pos, R, 4, "row_pos"), _buf(topk_w, R, 4, "topk_w"),
-        _buf(out, n_tokens * hidden, es, "out"), _stream(stream)), "moelora_combine")
+        n_tokens, hidden, top_k, dtype, _buf(ys, R * hidden, es, dev, "ys"),
+        _buf(row_pos, R, 4, dev, "row_pos"), _buf(topk_w, R, 4, dev, "topk_w"),
+        _buf(out, n_tokens * hidden, es, dev, "out"), st), "moelora_combine")
 
 
 def moelora_combine_backward(n_tokens, hidden, top_k, dtype, dout, ys, row_pos, topk_w, dys, dw,
                              stream=None):
+    st, dev = _where(stream)
     R, es = n_tokens * top_k, _es(dtype)
     _check(_lib.moelora_combine_backward(
-        n_tokens, hidden, top_k, dtype, _buf(dout, n_tokens * hidden, es, "dout"),
-        _buf(ys, R * hidden, es, "ys", dw is None), _buf(row_pos, R, 4, "row_pos"),
-        _buf(topk_w, R, 4, "topk_w", dys is None), _buf(dys, R * hidden, es, "dys", True),
-        _buf(dw, R, 4, "dw", True), _stream(stream)), "moelora_combine_backward")
+        n_tokens, hidden, top_k, dtype, _buf(dout, n_tokens * hidden, es, dev, "dout"),
+        _buf(ys, R * hidden, es, dev, "ys", dw is None), _buf(row_pos, R, 4, dev, "row_pos"),
+        _buf(topk_w, R, 4, dev, "topk_w", dys is None), _buf(dys, R * hidden, es, dev, "dys", True),
+        _buf(dw, R, 4, dev, "dw", True), st), "moelora_combine_backward")
 
 
 def moelora_quantize_rows(n_rows, width, dtype, x, n_src, rows, row_div, codes, scales,
                           stream=None):
+    st, dev = _where(stream)
     kb = (width + 127) // 128
     _check(_lib.moelora_quantize_rows(
-        n_rows, width, dtype, _buf(x, n_src * width, _es(dtype), "x"), n_src,
-        _buf(rows, n_rows, 4, "rows", True), row_div, _buf(codes, n_rows * kb * 128, 1, "codes"),
-        _buf(scales, n_rows * kb, 4, "scales"), _stream(stream)), "moelora_quantize_rows")
+        n_rows, width, dtype, _buf(x, n_src * width, _es(dtype), dev, "x"), n_src,
+        _buf(rows, n_rows, 4, dev, "rows", True), row_div, _buf(codes, n_rows * kb * 128, 1, dev, "codes"),
+        _buf(scales, n_rows * kb, 4, dev, "scales"), st), "moelora_quantize_rows")
 
 
 def moelora_quantize_weights(n_mats, rows, width, dtype, w, codes, scales, codes_t=None,
                              scales_t=None, stream=None):
+    st, dev = _where(stream)
     kb, nb = (width + 127) // 128, (rows + 127) // 128
     _check(_lib.moelora_quantize_weights(
-        n_mats, rows, width, dtype, _buf(w, n_mats * rows * width, _es(dtype), "w"),
-        _buf(codes, n_mats * rows * kb * 128, 1, "codes"),
-        _buf(scales, n_mats * nb * kb, 4, "scales"),
-        _buf(codes_t, n_mats * width * nb * 128, 1, "codes_t", True),
-        _buf(scales_t, n_mats * nb * kb, 4, "scales_t", True), _stream(stream)),
+        n_mats, rows, width, dtype, _buf(w, n_mats * rows * width, _es(dtype), dev, "w"),
+        _buf(codes, n_mats * rows * kb * 128, 1, dev, "codes"),
+        _buf(scales, n_mats * nb * kb, 4, dev, "scales"),
+        _buf(codes_t, n_mats * width * nb * 128, 1, dev, "codes_t", True),
+        _buf(scales_t, n_mats * nb * kb, 4, dev, "scales_t", True), st),
         "moelora_quantize_weights")
 
 
 def moelora_fp8_gemm(n_rows, n_out, width, n_experts, out_dtype, flags, codes, scales,
                      expert_start, w_codes, w_scales, out, stream=None):
+    st, dev = _where(stream)
     kb, nb = (width + 127) // 128, (n_out + 127) // 128
     mats = n_experts * (2 if flags & FP8_SILU_MUL else 1)
     _check(_lib.moelora_fp8_gemm(
         n_rows, n_out, width, n_experts, out_dtype, flags,
-        _buf(codes, n_rows * kb * 128, 1, "codes"), _buf(scales, n_rows * kb, 4, "scales"),
-        _buf(expert_start, n_experts + 1, 4, "expert_start", True),
-        _buf(w_codes, mats * n_out * kb * 128, 1, "w_codes"),
-        _buf(w_scales, mats * nb * kb, 4, "w_scales"),
-        _buf(out, n_rows * n_out, _es(out_dtype), "out"), _stream(stream)), "moelora_fp8_gemm")
+        _buf(codes, n_rows * kb * 128, 1, dev, "codes"), _buf(scales, n_rows * kb, 4, dev, "scales"),
+        _buf(expert_start, n_experts + 1, 4, dev, "expert_start", True),
+        _buf(w_codes, mats * n_out * kb * 128, 1, dev, "w_codes"),
+        _buf(w_scales, mats * nb * kb, 4, dev, "w_scales"),
+        _buf(out, n_rows * n_out, _es(out_dtype), dev, "out"), st), "moelora_fp8_gemm")
 
 
 class Plan:

@@ -82,6 +82,9 @@ __device__ __forceinline__ void store4(OT *row, int n, int N, const float *v) {
   }
 }
 
+// s_waitcnt operand that waits for all but the n newest vector loads.
+constexpr int wait_vmcnt(int n) { return 0x0f70 | (n & 15) | (n >> 4) << 14; }
+
 // start[] entries are device data: clamped into [0, R].
 __device__ __forceinline__ int row_bound(const int *start, int e, int R) {
   return min(max(start[e], 0), R);
@@ -89,18 +92,29 @@ __device__ __forceinline__ int row_bound(const int *start, int e, int R) {
 
 // ---------------------------------------------------------------- few rows
 //
-// A workgroup owns NT 16-row weight tiles (per half) of one expert and up to
-// 16 TG of its rows at a time; its four waves take every fourth block of the
-// contraction and add their sums through LDS in wave order.  Weights go from
-// HBM straight into the operand registers, a whole 128-byte line per row and
-// block, non-temporal; kUnroll blocks are loaded before the first is used.
+// A workgroup owns 16 NT weight rows (of each half) of one expert and up to
+// 16 TG of its tokens at a time; its four waves take every fourth block of
+// the contraction and add their sums through LDS in wave order, so that a
+// narrow product still fills the chip.  Each wave streams its weights through
+// an LDS ring of its own, S blocks deep, in whole 128-byte lines (8 lanes a
+// line): loaded straight into operand registers, 16 rows at 64 bytes an
+// instruction, the address unit and not HBM set the pace.  Tokens, few and
+// shared by all workgroups, come from cache into registers.
 constexpr int kSWaves = 4;
 constexpr int kSThreads = kSWaves * kWave;
 
-template <int NT, int TG, int U, bool SILU, typename OT>
+// LDS byte offset of 16-byte chunk c of a 128-byte row: 16 consecutive rows
+// read at one chunk fall on 16 distinct bank groups.
+__device__ __forceinline__ int lds_off(int row, int c) {
+  return row * 128 + ((c ^ ((row >> 1) & 7)) << 4);
+}
+
+template <int NT, int TG, int S, bool SILU, typename OT>
 __global__ __launch_bounds__(kSThreads) void k_fp8_stream(Fp8GemmArgs a) {
   constexpr int HV = SILU ? 2 : 1, A = HV * NT;
+  constexpr int SLOT = A * 16 * 128;
   typedef Block<sizeof(OT) == 4> B;
+  extern __shared__ __align__(16) unsigned char smem[];
   __shared__ f32x4_t red[kSWaves][A * TG][kWave];
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -128,16 +142,22 @@ __global__ __launch_bounds__(kSThreads) void k_fp8_stream(Fp8GemmArgs a) {
     lo = row_bound(a.start, e, a.R), hi = row_bound(a.start, e + 1, a.R);
   }
   if (lo >= hi) return;
-  const int n0 = blockIdx.x * NT * 16;
-  const uint8_t *wp[A];
-  const float *sp[A];
+  const int KB = a.KB, n0 = blockIdx.x * NT * 16, cols = min(NT * 16, a.N - n0);
+  const size_t mat = (size_t)e * HV;
+  const uint8_t *wbase[2] = {a.w + (mat * a.N + n0) * a.P, a.w + ((mat + HV - 1) * a.N + n0) * a.P};
+  uint32_t woff[8];
 #pragma unroll
-  for (int i = 0; i < A; ++i) {
-    const int half = i / NT, n = n0 + (i % NT) * 16;
-    const size_t mat = (size_t)e * HV + half;
-    wp[i] = a.w + (mat * a.N + min(n + l16, a.N - 1)) * a.P + g * 16;
-    sp[i] = a.ws + (mat * a.NB + min(n / 128, a.NB - 1)) * a.KB;
+  for (int j = 0; j < 2 * NT; ++j) {
+    const int r = 8 * j + (lane >> 3);
+    woff[j] = (uint32_t)(r * a.P) + 16 * ((lane & 7) ^ ((r >> 1) & 7));
   }
+  // weight scales 64 blocks at a time, one a lane (the workgroup's columns lie
+  // in one block of 128)
+  static_assert(NT <= 4 && 16 % S == 0, "");
+  const float *wsp = a.ws + (mat * a.NB + n0 / 128) * KB;
+  float ws[HV];
+  unsigned char *const ring = smem + wave * (S * SLOT);
+
   for (int m0 = lo; m0 < hi; m0 += 16 * TG) {
     f32x4_t acc[A][TG];
 #pragma unroll
@@ -151,48 +171,72 @@ __global__ __launch_bounds__(kSThreads) void k_fp8_stream(Fp8GemmArgs a) {
       xr[t] = min(m0 + 16 * t + l16, hi - 1);  // (rows past the last repeat it and are dropped)
       xp[t] = a.x + (size_t)xr[t] * a.P + g * 16;
     }
-    for (int b0 = wave; b0 < a.KB; b0 += kSWaves * U) {
-      u32x4_t w0[U][A], w1[U][A], x0[U][TG], x1[U][TG];
-      float sx[U][TG], sw[U][A];
+    u32x4_t x0[S][TG], x1[S][TG];
+    float sx[S][TG];
+    // block b into slot u: weights by direct loads to LDS (past the last
+    // block from an empty resource: they fetch nothing), tokens into registers
+    auto issue = [&](int u, int b) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int b = b0 + u * kSWaves;
-        if (b < a.KB) {
-          const size_t off = (size_t)b * 128;
+      for (int h = 0; h < HV; ++h) {
+        const __amdgpu_buffer_rsrc_t res = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<uint8_t *>(wbase[h]), (short)0, b < KB ? (int)(cols * a.P) : 0, kBufferWord3);
 #pragma unroll
-          for (int i = 0; i < A; ++i) {
-            w0[u][i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t *>(wp[i] + off));
-            w1[u][i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t *>(wp[i] + off + 64));
-            sw[u][i] = sp[i][b];
-          }
+        for (int j = 0; j < 2 * NT; ++j)
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(
+              res, (__attribute__((address_space(3))) void *)(ring + u * SLOT + (h * NT * 16 + 8 * j) * 128),
+              16, woff[j], b * 128, 0, kCpolNonTemporal);
+      }
+      const int bc = min(b, KB - 1);
 #pragma unroll
-          for (int t = 0; t < TG; ++t) {
-            x0[u][t] = *reinterpret_cast<const u32x4_t *>(xp[t] + off);
-            x1[u][t] = *reinterpret_cast<const u32x4_t *>(xp[t] + off + 64);
-            sx[u][t] = a.xs[(size_t)b * a.R + xr[t]];
-          }
-        }
+      for (int t = 0; t < TG; ++t) {
+        x0[u][t] = *reinterpret_cast<const u32x4_t *>(xp[t] + (size_t)bc * 128);
+        x1[u][t] = *reinterpret_cast<const u32x4_t *>(xp[t] + (size_t)bc * 128 + 64);
+        sx[u][t] = a.xs[(size_t)bc * a.R + xr[t]];
+      }
+    };
+#pragma unroll
+    for (int u = 0; u < S; ++u) issue(u, wave + u * kSWaves);
+    for (int b0 = wave; b0 < KB; b0 += kSWaves * S) {
+      if (b0 % kWave == wave) {
+#pragma unroll
+        for (int h = 0; h < HV; ++h)
+          ws[h] = wsp[(size_t)h * a.NB * KB + min(b0 - wave + lane, KB - 1)];
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (b0 + u * kSWaves < a.KB) {
+      for (int u = 0; u < S; ++u) {
+        const int b = b0 + u * kSWaves;
+        // loads return in order: no more than the S - 1 later blocks' weight
+        // loads may be in flight when this block is read
+        __builtin_amdgcn_s_waitcnt(wait_vmcnt((S - 1) * 2 * A));
+        __builtin_amdgcn_sched_barrier(0);
+        if (b < KB) {
+          const unsigned char *st = ring + u * SLOT;
+          float sw[HV];
+#pragma unroll
+          for (int h = 0; h < HV; ++h)
+            sw[h] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ws[h]), b % kWave));
           typename B::Operand w[A];
 #pragma unroll
-          for (int i = 0; i < A; ++i) w[i] = B::load(w0[u][i], w1[u][i]);
+          for (int i = 0; i < A; ++i)
+            w[i] = B::load(*reinterpret_cast<const u32x4_t *>(st + lds_off(16 * i + l16, g)),
+                           *reinterpret_cast<const u32x4_t *>(st + lds_off(16 * i + l16, g + 4)));
 #pragma unroll
           for (int t = 0; t < TG; ++t) {
             const typename B::Operand x = B::load(x0[u][t], x1[u][t]);
 #pragma unroll
             for (int i = 0; i < A; ++i) {
               const f32x4_t p = B::mma(w[i], x);
-              const float s = sx[u][t] * sw[u][i];
+              const float s = sx[u][t] * sw[i / NT];
 #pragma unroll
               for (int v = 0; v < 4; ++v) acc[i][t][v] = fmaf(s, p[v], acc[i][t][v]);
             }
           }
         }
+        __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): the slot is read out
+        issue(u, b + kSWaves * S);
       }
     }
+    __builtin_amdgcn_s_waitcnt(0x0f70);  // no load outlives its slot
 #pragma unroll
     for (int i = 0; i < A; ++i)
 #pragma unroll
@@ -241,13 +285,7 @@ __global__ __launch_bounds__(kSThreads) void k_fp8_stream(Fp8GemmArgs a) {
 // and weight rows past N, lie past their buffer resource's end: their loads
 // fetch nothing, and their outputs are dropped.
 constexpr int kGWaves = 4, kGThreads = kGWaves * kWave;
-constexpr int kGW = 64 * kGWaves;
 constexpr int kGSlots = 2;              // stages of tokens
-constexpr int kGWaveW = 64 * 128;        // LDS bytes of a wave's weights
-
-__device__ __forceinline__ int lds_off(int row, int c) {
-  return row * 128 + ((c ^ ((row >> 1) & 7)) << 4);
-}
 
 struct RowTile {
   int e, m0, hi, nt;  // e < 0: nothing to do
@@ -299,10 +337,11 @@ __device__ __forceinline__ RowTile find_tile(const Fp8GemmArgs &a, int BM, int n
   return {e, lo + r % nb * BM, hi, r / nb};
 }
 
-template <int TT, bool SILU, typename OT>
-__global__ __launch_bounds__(kGThreads, 2) void k_fp8_tiled(Fp8GemmArgs a, int ncols) {
+template <int WT, int TT, bool SILU, typename OT>
+__global__ __launch_bounds__(kGThreads, sizeof(OT) == 2 && WT * TT <= 8 ? 3 : 2) void k_fp8_tiled(Fp8GemmArgs a, int ncols) {
   extern __shared__ __align__(16) unsigned char smem[];
-  constexpr int HV = SILU ? 2 : 1, COLS = kGW / HV, WC = 64 / HV;  // columns a workgroup, a wave
+  constexpr int HV = SILU ? 2 : 1, WC = 16 * WT / HV, COLS = kGWaves * WC;  // columns a wave, a workgroup
+  constexpr int WH = WT / HV;           // weight tiles of a half
   constexpr int GM = 16 * TT, STAGE = GM * 128 + 512;
   constexpr int XL = GM / 8 / kGWaves;  // token loads a wave and slab
   typedef Block<sizeof(OT) == 4> B;
@@ -338,13 +377,13 @@ __global__ __launch_bounds__(kGThreads, 2) void k_fp8_tiled(Fp8GemmArgs a, int n
     const int r = 8 * (XL * wave + j) + (lane >> 3);
     xoff[j] = (uint32_t)(r * P) + 16 * ((lane & 7) ^ ((r >> 1) & 7));
   }
-  unsigned char *const wst = smem + kGSlots * STAGE + wave * kGWaveW;
+  unsigned char *const wst = smem + kGSlots * STAGE + wave * (WT * 16 * 128);
   struct Weights {
-    typename Block<false>::Operand v[4];
+    typename Block<false>::Operand v[WT];
   };
   auto issue_w = [&](int b) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < 2 * WT; ++j) {
       const __amdgpu_buffer_rsrc_t res = resource(wbase[j * 8 / WC], (int)(cols * P), b);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
           res, (__attribute__((address_space(3))) void *)(wst + 8 * j * 128), 16, woff[j % (WC / 8)],
@@ -353,7 +392,7 @@ __global__ __launch_bounds__(kGThreads, 2) void k_fp8_tiled(Fp8GemmArgs a, int n
   };
   auto read_w = [&](Weights &w) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < WT; ++i)
       w.v[i] = {*reinterpret_cast<const u32x4_t *>(wst + lds_off(16 * i + l16, g)),
                 *reinterpret_cast<const u32x4_t *>(wst + lds_off(16 * i + l16, g + 4))};
   };
@@ -376,30 +415,30 @@ __global__ __launch_bounds__(kGThreads, 2) void k_fp8_tiled(Fp8GemmArgs a, int n
   const float *wsp = a.ws + (mat * a.NB + min((n0 + WC * wave) / 128, a.NB - 1)) * KB;
   float ws[HV];
 
-  f32x4_t acc[4][TT];
+  f32x4_t acc[WT][TT];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < WT; ++i)
 #pragma unroll
     for (int t = 0; t < TT; ++t) acc[i][t] = f32x4_t{0, 0, 0, 0};
 
   // block sums not yet added, and their scales
-  f32x4_t p[4];
+  f32x4_t p[WT];
   float s[HV];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) p[i] = f32x4_t{0, 0, 0, 0};
+  for (int i = 0; i < WT; ++i) p[i] = f32x4_t{0, 0, 0, 0};
 #pragma unroll
   for (int h = 0; h < HV; ++h) s[h] = 0.f;
   auto add = [&](int i, int t) {
 #pragma unroll
-    for (int v = 0; v < 4; ++v) acc[i][t][v] = fmaf(s[SILU ? i / 2 : 0], p[i][v], acc[i][t][v]);
+    for (int v = 0; v < 4; ++v) acc[i][t][v] = fmaf(s[SILU ? i / WH : 0], p[i][v], acc[i][t][v]);
   };
 
   // Slab b with its weights in `w`; reads slab b + 1's into `wn` half way.
   // The waits count this wave's own loads in their order of issue: tokens of
-  // b + 1 (XL + 1 loads, top of slab b), weights of b + 2 (8 loads, middle of
+  // b + 1 (XL + 1 loads, top of slab b), weights of b + 2 (2 WT loads, middle of
   // slab b); nothing moves across the barrier or the waits.
   auto step = [&](int b, const Weights &w, Weights &wn) {
-    __builtin_amdgcn_s_waitcnt(0x0f70 | 8);  // tokens of b landed; weights of b + 1 may not have
+    __builtin_amdgcn_s_waitcnt(0x0f70 | (2 * WT));  // tokens of b landed; weights of b + 1 may not have
     __builtin_amdgcn_s_barrier();            // ... for every wave, and slab b - 1 is read out
     if (b % kWave == 0) {
 #pragma unroll
@@ -412,9 +451,9 @@ __global__ __launch_bounds__(kGThreads, 2) void k_fp8_tiled(Fp8GemmArgs a, int n
 #pragma unroll
     for (int h = 0; h < HV; ++h)
       sw[h] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ws[h]), b % kWave));
-    typename B::Operand wo[4];
+    typename B::Operand wo[WT];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) wo[i] = B::load(w.v[i].lo, w.v[i].hi);
+    for (int i = 0; i < WT; ++i) wo[i] = B::load(w.v[i].lo, w.v[i].hi);
     // token fragments one group ahead of their MFMAs; the scheduling barrier
     // keeps the compiler from reading all groups at once (registers)
     auto read_x = [&](int t, u32x4_t &lo, u32x4_t &hi) {
@@ -430,9 +469,9 @@ __global__ __launch_bounds__(kGThreads, 2) void k_fp8_tiled(Fp8GemmArgs a, int n
       const float sxt = sx[16 * t + l16];
       const typename B::Operand x = B::load(xlo[t & 1], xhi[t & 1]);
       // a block sum is scaled and added just before its register takes the
-      // next group's: four MFMAs later, so nothing waits for the matrix core
+      // next group's: WT MFMAs later, so nothing waits for the matrix core
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < WT; ++i) {
         add(i, t == 0 ? TT - 1 : t - 1);
         p[i] = B::mma(wo[i], x);
         __builtin_amdgcn_sched_barrier(0);
@@ -465,7 +504,7 @@ __global__ __launch_bounds__(kGThreads, 2) void k_fp8_tiled(Fp8GemmArgs a, int n
   }
   if (b < KB) step(b, wa, wb);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) add(i, TT - 1);
+  for (int i = 0; i < WT; ++i) add(i, TT - 1);
   __builtin_amdgcn_s_waitcnt(0x0f70);  // no load of this workgroup outlives it
 
 #pragma unroll
@@ -474,28 +513,33 @@ __global__ __launch_bounds__(kGThreads, 2) void k_fp8_tiled(Fp8GemmArgs a, int n
     if (m >= rows) continue;
     OT *row = static_cast<OT *>(a.out) + (size_t)(rt.m0 + m) * a.N;
 #pragma unroll
-    for (int i = 0; i < (SILU ? 2 : 4); ++i) {
+    for (int i = 0; i < WH; ++i) {
       const int n = n0 + WC * wave + 16 * i + 4 * g;
       if (n >= a.N) continue;
       float o[4];
 #pragma unroll
-      for (int v = 0; v < 4; ++v) o[v] = SILU ? silu_f32(acc[i][t][v]) * acc[(i + 2) & 3][t][v] : acc[i][t][v];
+      for (int v = 0; v < 4; ++v) o[v] = SILU ? silu_f32(acc[i][t][v]) * acc[(i + WH) % WT][t][v] : acc[i][t][v];
       store4<OT>(row, n, a.N, o);
     }
   }
 }
 
-template <int NT, int TG, int U, bool SILU, typename OT>
+template <int NT, int TG, int S, bool SILU, typename OT>
 hipError_t stream_t(const Fp8GemmArgs &a, hipStream_t st) {
-  return launch_kernel(k_fp8_stream<NT, TG, U, SILU, OT>,
-                       dim3((a.N + 16 * NT - 1) / (16 * NT), a.E < a.R ? a.E : a.R), dim3(kSThreads), 0,
-                       st, a);
+  constexpr int LDS = kSWaves * S * NT * (SILU ? 2 : 1) * 16 * 128;
+  auto kern = k_fp8_stream<NT, TG, S, SILU, OT>;
+  hipError_t err = hipFuncSetAttribute(reinterpret_cast<const void *>(kern),
+                                       hipFuncAttributeMaxDynamicSharedMemorySize, LDS);
+  if (err != hipSuccess) return err;
+  return launch_kernel(kern, dim3((a.N + 16 * NT - 1) / (16 * NT), a.E < a.R ? a.E : a.R),
+                       dim3(kSThreads), LDS, st, a);
 }
 
-template <int TT, bool SILU, typename OT>
+template <int WT, int TT, bool SILU, typename OT>
 hipError_t tiled_t(const Fp8GemmArgs &a, hipStream_t st) {
-  constexpr int COLS = kGW / (SILU ? 2 : 1), GM = 16 * TT, LDS = kGSlots * (GM * 128 + 512) + kGWaves * kGWaveW;
-  auto kern = k_fp8_tiled<TT, SILU, OT>;
+  constexpr int COLS = kGWaves * 16 * WT / (SILU ? 2 : 1), GM = 16 * TT;
+  constexpr int LDS = kGSlots * (GM * 128 + 512) + kGWaves * 16 * WT * 128;
+  auto kern = k_fp8_tiled<WT, TT, SILU, OT>;
   hipError_t err = hipFuncSetAttribute(reinterpret_cast<const void *>(kern),
                                        hipFuncAttributeMaxDynamicSharedMemorySize, LDS);
   if (err != hipSuccess) return err;
@@ -508,11 +552,14 @@ hipError_t tiled_t(const Fp8GemmArgs &a, hipStream_t st) {
 template <bool SILU, typename OT>
 hipError_t gemm_t(const Fp8GemmArgs &a, hipStream_t st) {
   const int mean = a.R / (a.E < a.R ? a.E : a.R);  // rows an expert, if all are hit
-  if (mean <= 8) return stream_t<SILU ? 1 : 2, 1, 4, SILU, OT>(a, st);
-  if (mean <= 24) return stream_t<SILU ? 1 : 2, 2, 2, SILU, OT>(a, st);
-  if (mean <= 64) return stream_t<SILU ? 1 : 2, 4, 2, SILU, OT>(a, st);
+#ifdef FORCE
+  return FORCE;
+#endif
+  if (mean <= 8) return stream_t<SILU ? 1 : 2, 1, 2, SILU, OT>(a, st);
+  if (mean <= 16) return tiled_t<2, 2, SILU, OT>(a, st);
+  if (mean <= 64) return tiled_t<2, 4, SILU, OT>(a, st);
   // float32 results: widened operands leave registers for 64 rows
-  return tiled_t<sizeof(OT) == 4 ? 4 : 8, SILU, OT>(a, st);
+  return tiled_t<4, sizeof(OT) == 4 ? 4 : 8, SILU, OT>(a, st);
 }
 
 }  // namespace
