@@ -24,36 +24,70 @@ constexpr int kBlk = 128;    // elements a scale
 constexpr int kLanes = 16;   // lanes on a block, 8 elements each
 constexpr int kGroups = kThreads / kLanes;
 
-// Eight elements of a row of K from element c on, zeros past K.
+// Eight elements of a row of K from element c on, zeros past K, as they are
+// stored (bf16: two a dword).
+template <typename DT> struct Raw8;
+template <> struct Raw8<uint16_t> {
+  u32x4_t v;
+};
+template <> struct Raw8<float> {
+  u32x4_t v[2];
+};
 template <typename DT, bool VEC>
-__device__ __forceinline__ void load8(const DT *row, int c, int K, float *f) {
+__device__ __forceinline__ Raw8<DT> load8(const DT *row, int c, int K) {
   if constexpr (VEC && sizeof(DT) == 2) {
-    u32x4_t v = c < K ? *reinterpret_cast<const u32x4_t *>(row + c) : u32x4_t{0, 0, 0, 0};
-    const Chunk<uint16_t> h = chunk_elems<uint16_t>(v);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = bf16_to_f32(h.v[i]);
+    return {c < K ? *reinterpret_cast<const u32x4_t *>(row + c) : u32x4_t{0, 0, 0, 0}};
   } else if constexpr (VEC) {
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const f32x4_t v = c + 4 * q < K ? *reinterpret_cast<const f32x4_t *>(row + c + 4 * q)
-                                      : f32x4_t{0, 0, 0, 0};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) f[4 * q + i] = v[i];
-    }
+    return {{c < K ? *reinterpret_cast<const u32x4_t *>(row + c) : u32x4_t{0, 0, 0, 0},
+             c + 4 < K ? *reinterpret_cast<const u32x4_t *>(row + c + 4) : u32x4_t{0, 0, 0, 0}}};
   } else {
+    struct Eight {
+      DT e[8];
+    } f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = c + i < K ? Elem<DT>::to_f32(row[c + i]) : 0.f;
+    for (int i = 0; i < 8; ++i) f.e[i] = c + i < K ? row[c + i] : DT(0);
+    return __builtin_bit_cast(Raw8<DT>, f);
   }
 }
 
-// Largest finite magnitude, as the bits of a non-negative float.
-__device__ __forceinline__ uint32_t amax_bits8(const float *f) {
+__device__ __forceinline__ void to_f32(const Raw8<uint16_t> &r, float *f) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(r.v[i] << 16);
+    f[2 * i + 1] = __uint_as_float(r.v[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void to_f32(const Raw8<float> &r, float *f) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(r.v[i / 4][i % 4]);
+}
+
+// Largest magnitude of the eight as the bits of a non-negative float; not
+// finite if any of them is not.  bf16: both halves of a dword at once.
+typedef unsigned short u16x2_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t amax_bits8(const Raw8<uint16_t> &r) {
+  u16x2_t m = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2_t, r.v[i] & 0x7fff7fffu));
+  return (uint32_t)max(m[0], m[1]) << 16;
+}
+__device__ __forceinline__ uint32_t amax_bits8(const Raw8<float> &r) {
   uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t b = __float_as_uint(f[i]) & 0x7fffffffu;
-    m = max(m, b < 0x7f800000u ? b : 0u);
-  }
+  for (int i = 0; i < 8; ++i) m = max(m, r.v[i / 4][i % 4] & 0x7fffffffu);
+  return m;
+}
+constexpr uint32_t kInfBits = 0x7f800000u;
+__device__ __forceinline__ bool finite(float v) { return (__float_as_uint(v) & 0x7fffffffu) < kInfBits; }
+// ... of the finite ones only.
+template <typename DT>
+__device__ __forceinline__ uint32_t amax_finite8(const Raw8<DT> &r) {
+  float f[8];
+  to_f32(r, f);
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, finite(f[i]) ? __float_as_uint(f[i]) & 0x7fffffffu : 0u);
   return m;
 }
 
@@ -65,18 +99,24 @@ __device__ __forceinline__ int scale_exp(uint32_t amax) {
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
-__device__ __forceinline__ uint32_t codes4(const float *f, float inv) {
-  float g[4];
+// Codes of the eight times inv.  `odd`: some element of the block is not
+// finite (its code is set by hand).
+template <typename DT>
+__device__ __forceinline__ uint2 codes8(const Raw8<DT> &r, float inv, bool odd) {
+  float f[8];
+  to_f32(r, f);
+  uint32_t u[2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) g[i] = f[i] * inv;
-  int w = __builtin_amdgcn_cvt_pk_fp8_f32(g[0], g[1], 0, false);
-  w = __builtin_amdgcn_cvt_pk_fp8_f32(g[2], g[3], w, true);
-  uint32_t u = (uint32_t)w;
+  for (int h = 0; h < 2; ++h) {
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * h] * inv, f[4 * h + 1] * inv, 0, false);
+    u[h] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f[4 * h + 2] * inv, f[4 * h + 3] * inv, w, true);
+  }
+  if (odd) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if ((__float_as_uint(f[i]) & 0x7fffffffu) >= 0x7f800000u)
-      u = (u & ~(0xffu << 8 * i)) | (0x7fu << 8 * i);
-  return u;
+    for (int i = 0; i < 8; ++i)
+      if (!finite(f[i])) u[i / 4] = (u[i / 4] & ~(0xffu << 8 * (i % 4))) | (0x7fu << 8 * (i % 4));
+  }
+  return make_uint2(u[0], u[1]);
 }
 
 // 16 rows a workgroup, up to kUnroll blocks of each: 16 lanes a (row, block).
@@ -98,19 +138,24 @@ __global__ __launch_bounds__(kThreads) void k_quant_rows(QuantRowsArgs a, int KB
   uint8_t *out = a.codes + (size_t)r * KB * kBlk;
   const int b_end = min(KB, ((int)blockIdx.y + 1) * per_wg);
   for (int b0 = blockIdx.y * per_wg; b0 < b_end; b0 += kUnroll) {
-    float f[kUnroll][8];
+    Raw8<DT> v[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u)
-      if (b0 + u < b_end) load8<DT, VEC>(row, (b0 + u) * kBlk + l * 8, a.K, f[u]);
+      if (b0 + u < b_end) v[u] = load8<DT, VEC>(row, (b0 + u) * kBlk + l * 8, a.K);
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       if (b0 + u >= b_end) break;
-      uint32_t m = amax_bits8(f[u]);
+      uint32_t m = amax_bits8(v[u]);
 #pragma unroll
       for (int d = 1; d < kLanes; d <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
+      const bool odd = m >= kInfBits;  // the same for the block's 16 lanes
+      if (odd) {
+        m = amax_finite8(v[u]);
+#pragma unroll
+        for (int d = 1; d < kLanes; d <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
+      }
       const int e = scale_exp(m);
-      const float inv = pow2(-e);
-      const uint2 c = make_uint2(codes4(f[u], inv), codes4(f[u] + 4, inv));
+      const uint2 c = codes8(v[u], pow2(-e), odd);
       *reinterpret_cast<uint2 *>(out + (size_t)(b0 + u) * kBlk + l * 8) = c;
       if (l == 0) a.scales[(size_t)(b0 + u) * a.M + r] = pow2(e);
     }
@@ -131,26 +176,33 @@ __global__ __launch_bounds__(kThreads) void k_quant_weights(QuantWeightsArgs a, 
   const DT *w = static_cast<const DT *>(a.w) + (size_t)mat * a.N * a.K;
   const int n0 = nb * kBlk, k0 = kb * kBlk;
   constexpr int kPass = kBlk / kGroups;
-  float f[kPass][8];
-  uint32_t m = 0;
+  Raw8<DT> v[kPass];
 #pragma unroll
   for (int i = 0; i < kPass; ++i) {
     const int n = n0 + i * kGroups + g;
-    if (n < a.N) {
-      load8<DT, VEC>(w + (size_t)n * a.K, k0 + l * 8, a.K, f[i]);
-    } else {
-#pragma unroll
-      for (int q = 0; q < 8; ++q) f[i][q] = 0.f;
-    }
+    v[i] = load8<DT, VEC>(w + (size_t)min(n, a.N - 1) * a.K, k0 + l * 8, n < a.N ? a.K : 0);
   }
+  auto block_max = [&](uint32_t m) {
 #pragma unroll
-  for (int i = 0; i < kPass; ++i) m = max(m, amax_bits8(f[i]));
+    for (int d = 1; d < kWave; d <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
+    if (tid % kWave == 0) wmax[tid / kWave] = m;
+    __syncthreads();
 #pragma unroll
-  for (int d = 1; d < kWave; d <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
-  if (tid % kWave == 0) wmax[tid / kWave] = m;
-  __syncthreads();
+    for (int q = 0; q < kThreads / kWave; ++q) m = max(m, wmax[q]);
+    return m;
+  };
+  uint32_t m = 0;
 #pragma unroll
-  for (int v = 0; v < kThreads / kWave; ++v) m = max(m, wmax[v]);
+  for (int i = 0; i < kPass; ++i) m = max(m, amax_bits8(v[i]));
+  m = block_max(m);
+  const bool odd = m >= kInfBits;  // the same for the whole workgroup
+  if (odd) {
+    __syncthreads();
+    m = 0;
+#pragma unroll
+    for (int i = 0; i < kPass; ++i) m = max(m, amax_finite8(v[i]));
+    m = block_max(m);
+  }
   const int e = scale_exp(m);
   const float inv = pow2(-e);
   if (tid == 0) {
@@ -160,7 +212,7 @@ __global__ __launch_bounds__(kThreads) void k_quant_weights(QuantWeightsArgs a, 
 #pragma unroll
   for (int i = 0; i < kPass; ++i) {
     const int nl = i * kGroups + g, n = n0 + nl;
-    const uint2 c = make_uint2(codes4(f[i], inv), codes4(f[i] + 4, inv));
+    const uint2 c = codes8(v[i], inv, odd);
     if (n < a.N) *reinterpret_cast<uint2 *>(a.codes + ((size_t)mat * a.N + n) * P + k0 + l * 8) = c;
     if (a.codes_t) {
       uint32_t *t = reinterpret_cast<uint32_t *>(tile + nl * kPitch + l * 8);

@@ -549,17 +549,70 @@ hipError_t tiled_t(const Fp8GemmArgs &a, hipStream_t st) {
   return launch_kernel(kern, dim3(round_up8(tiles * ncols)), dim3(kGThreads), LDS, st, a, ncols);
 }
 
+// Most workgroups a tiled launch can hold: row tiles of GM rows (each expert's
+// last one short) times column tiles.
+long long tiled_wgs(const Fp8GemmArgs &a, bool silu, int WT, int TT) {
+  const long long GM = 16 * TT, cols = kGWaves * 16 * WT / (silu ? 2 : 1);
+  const long long ne = a.E < a.R ? a.E : a.R;
+  return (a.R + ne * (GM - 1)) / GM * ((a.N + cols - 1) / cols);
+}
+
+// Which kernel, by the mean rows of an expert and by how many workgroups a
+// tile leaves (two of 128 tokens x 256 weight rows fit a CU: 512 on the
+// chip).  us on one box, E = 32, top-4, 2880 -> 2 x 2880 with SILU ("g", by
+// tokens), and dense 4096 -> 11008 ("d", by rows):
+//            few rows      tiles: weight tiles of a wave x token tiles
+//            1x16  2x16    2x2   2x4   2x8   4x8
+//   g32      73    81      87    89    89   106
+//   g64      97    93      97    94    97   110
+//   g256    257   184     115   109   109   117
+//   g512    481   312     151   126   121   119
+//   g1024   944   585     215   169   147   142
+//   d16      13    14      18    18    22    32
+//   d32      22    16      18    18    22    32
+//   d64      42    29      18    19    23    33
+//   d512    328   217      49    34    35    37
+//   d1024   663   435      90    66    53    58
 template <bool SILU, typename OT>
 hipError_t gemm_t(const Fp8GemmArgs &a, hipStream_t st) {
   const int mean = a.R / (a.E < a.R ? a.E : a.R);  // rows an expert, if all are hit
 #ifdef FORCE
   return FORCE;
 #endif
-  if (mean <= 8) return stream_t<SILU ? 1 : 2, 1, 2, SILU, OT>(a, st);
-  if (mean <= 16) return tiled_t<2, 2, SILU, OT>(a, st);
-  if (mean <= 64) return tiled_t<2, 4, SILU, OT>(a, st);
-  // float32 results: widened operands leave registers for 64 rows
-  return tiled_t<4, sizeof(OT) == 4 ? 4 : 8, SILU, OT>(a, st);
+  constexpr int NT = SILU ? 1 : 2;  // 32 weight rows a workgroup either way
+  // (several experts: some have twice the mean, and pass their weights twice)
+  if (mean <= (a.E == 1 ? 16 : 7)) return stream_t<NT, 1, 2, SILU, OT>(a, st);
+  if (a.E == 1 && mean <= 32) return stream_t<NT, 2, 2, SILU, OT>(a, st);
+  if constexpr (sizeof(OT) == 2) {
+    if (mean >= 56 && tiled_wgs(a, SILU, 4, 8) >= 512) return tiled_t<4, 8, SILU, OT>(a, st);
+    if (mean >= 96 && tiled_wgs(a, SILU, 2, 8) >= 512) return tiled_t<2, 8, SILU, OT>(a, st);
+  } else {
+    // float32 results: widened operands leave registers for 64 tokens (the
+    // 25600-row gate_up 866 us against 919 with 2x4, g1024 201 against 198)
+    if (mean >= 192 && tiled_wgs(a, SILU, 4, 4) >= 512) return tiled_t<4, 4, SILU, OT>(a, st);
+  }
+  if (tiled_wgs(a, SILU, 2, 4) >= 160) return tiled_t<2, 4, SILU, OT>(a, st);
+  return tiled_t<2, 2, SILU, OT>(a, st);
+}
+
+// Every kernel gemm_t can pick (launch sites that only look kernels up).
+template <bool SILU, typename OT>
+hipError_t resolve_t() {
+  constexpr int NT = SILU ? 1 : 2;
+  Fp8GemmArgs a{};
+  a.R = a.N = a.K = a.E = a.KB = a.NB = 1, a.P = 128;
+  hipError_t e[6] = {stream_t<NT, 1, 2, SILU, OT>(a, nullptr), stream_t<NT, 2, 2, SILU, OT>(a, nullptr),
+                     tiled_t<2, 2, SILU, OT>(a, nullptr), tiled_t<2, 4, SILU, OT>(a, nullptr)};
+  if constexpr (sizeof(OT) == 2) {
+    e[4] = tiled_t<2, 8, SILU, OT>(a, nullptr);
+    e[5] = tiled_t<4, 8, SILU, OT>(a, nullptr);
+  } else {
+    e[4] = tiled_t<4, 4, SILU, OT>(a, nullptr);
+    e[5] = hipSuccess;
+  }
+  for (hipError_t r : e)
+    if (r != hipSuccess) return r;
+  return hipSuccess;
 }
 
 }  // namespace
@@ -570,13 +623,8 @@ hipError_t launch_fp8_gemm(const Fp8GemmArgs &a, bool silu, bool bf16, hipStream
 }
 
 hipError_t resolve_fp8_gemm(bool silu, bool bf16) {
-  for (int mean : {1, 16, 64, 1000}) {  // one row count of each kernel
-    Fp8GemmArgs a{};
-    a.R = mean, a.N = a.K = a.P = 128, a.E = a.KB = a.NB = 1;
-    const hipError_t e = launch_fp8_gemm(a, silu, bf16, nullptr);
-    if (e != hipSuccess) return e;
-  }
-  return hipSuccess;
+  if (silu) return bf16 ? resolve_t<true, uint16_t>() : resolve_t<true, float>();
+  return bf16 ? resolve_t<false, uint16_t>() : resolve_t<false, float>();
 }
 
 }  // namespace moelora

@@ -131,11 +131,12 @@ __global__ __launch_bounds__(kThreads) void k_order_count(int R, int E, int C,
 // the same expert find each other by ballots over the bits of the id, and a
 // lane's rank is the number of equal lanes below it.
 __global__ __launch_bounds__(kThreads) void k_order_place(
-    int R, int E, int C, int nch, int id_bits, const int *__restrict__ ids,
+    int R, int E, int C, int nch, int id_bits, int e_shift, const int *__restrict__ ids,
     const int *__restrict__ counts, int *__restrict__ expert_start, int *__restrict__ sorted_rows,
     int *__restrict__ row_pos) {
   __shared__ int next[kWaves][kMaxE];
   __shared__ int before[kMaxE];
+  __shared__ int part[2][kThreads];
   __shared__ int wsum[kWaves];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
   const int me = blockIdx.x;
@@ -148,17 +149,31 @@ __global__ __launch_bounds__(kThreads) void k_order_place(
     const int f = ids[q];
     if (held(f, E)) atomicAdd(&next[wave][f], 1);
   }
-  // totals, and the chunks before this one
+  // totals, and the chunks before this one: 2^e_shift experts at a time, the
+  // chunks dealt over the kThreads >> e_shift threads of an expert
+  const int per = 1 << e_shift, el = tid & (per - 1), gi = tid >> e_shift, G = kThreads >> e_shift;
   int kept = 0;
-  for (int e0 = 0; e0 < E; e0 += kThreads) {
-    const int e = e0 + tid;
+  for (int e0 = 0; e0 < E; e0 += per) {
+    const int e = tid < per ? e0 + tid : E;  // the expert this thread scans for
     int total = 0, mine = 0;
-    if (e < E) {
-      for (int c = 0; c < nch; ++c) {
-        const int n = counts[(size_t)c * E + e];
+    if (e0 + el < E) {
+#pragma unroll 4
+      for (int c = gi; c < nch; c += G) {
+        const int n = counts[(size_t)c * E + e0 + el];
         total += n;
         mine += c < me ? n : 0;
       }
+    }
+    if (G > 1) {
+      part[0][tid] = total;
+      part[1][tid] = mine;
+      __syncthreads();
+      total = mine = 0;
+      if (tid < per)
+        for (int q = 0; q < G; ++q) {
+          total += part[0][q * per + tid];
+          mine += part[1][q * per + tid];
+        }
     }
     int v = total;
 #pragma unroll
@@ -367,7 +382,8 @@ hipError_t dispatch_t(const OrderShape &s, size_t row_bytes, const void *x, cons
   while ((1 << bits) < s.E) ++bits;
   hipError_t e = launch_kernel(k_order_count, dim3(nch), dim3(kThreads), 0, st, s.R, s.E, C, ids, counts);
   if (e != hipSuccess) return e;
-  e = launch_kernel(k_order_place, dim3(nch), dim3(kThreads), 0, st, s.R, s.E, C, nch, bits, ids,
+  e = launch_kernel(k_order_place, dim3(nch), dim3(kThreads), 0, st, s.R, s.E, C, nch, bits,
+                    bits < 8 ? bits : 8, ids,
                     static_cast<const int *>(counts), expert_start, sorted_rows, row_pos);
   if (e != hipSuccess || !xs) return e;
   const RowGrid g = row_grid(s.T, chunks);

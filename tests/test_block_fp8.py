@@ -176,6 +176,31 @@ def test_quantize_weights(mats, N, K, dtype):
     assert torch.equal(only, codes)
 
 
+@pytest.mark.parametrize("dtype", [lib.F32, lib.BF16])
+def test_quantize_weights_special_values(dtype):
+    """Elements that are not finite get the NaN code in both copies and no say
+    in their block's scale; the other blocks do not notice."""
+    N, K = 140, 260
+    w = torch.from_numpy(spread(np.random.default_rng(1), 1, N, K)).to(DT[dtype])
+    w[0, 3, 7], w[0, 100, 130], w[0, 139, 259] = float("nan"), float("inf"), -float("inf")
+    w[0, 5, 9] = 1e30
+    codes, codes_t = (torch.zeros(1, a, up(b), dtype=torch.uint8, device="cuda") for a, b in ((N, K), (K, N)))
+    scales, scales_t = torch.zeros(1, 2, 3, device="cuda"), torch.zeros(1, 3, 2, device="cuda")
+    lib.moelora_quantize_weights(1, N, K, dtype, w.cuda(), codes, scales, codes_t, scales_t)
+    T, v = TABLE.numpy(), w[0].double().numpy()
+    got = T[codes[0, :, :K].cpu().numpy()]
+    assert np.array_equal(np.isnan(got), ~np.isfinite(v))
+    assert np.array_equal(codes[0, :, :K].cpu().numpy(), codes_t[0, :, :N].cpu().numpy().T)
+    for i in range(2):
+        for j in range(3):
+            blk = v[i * 128:i * 128 + 128, j * 128:j * 128 + 128]
+            s = scale_of(blk)
+            assert float(scales[0, i, j]) == s
+            fine = np.isfinite(blk)
+            want = T[codes_of(np.where(fine, blk, 0) / s)]
+            assert np.array_equal(got[i * 128:i * 128 + 128, j * 128:j * 128 + 128][fine], want[fine])
+
+
 # -------------------------------------------------------------- the product
 
 def make(counts, N, K, halves, seed, gap=0):
