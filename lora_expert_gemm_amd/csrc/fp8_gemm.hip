@@ -72,7 +72,10 @@ template <typename OT>
 __device__ __forceinline__ void store4(OT *row, int n, int N, const float *v) {
   OT o[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = Elem<OT>::from_f32(v[i]);
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(OT) == 2) o[i] = __builtin_bit_cast(uint16_t, (__bf16)v[i]);  // nearest even
+    else o[i] = v[i];
+  }
   if (N % 4 == 0) {  // (then n + 3 < N, and the four are aligned)
     if constexpr (sizeof(OT) == 2) *reinterpret_cast<uint2 *>(row + n) = __builtin_bit_cast(uint2, o);
     else *reinterpret_cast<u32x4_t *>(row + n) = __builtin_bit_cast(u32x4_t, o);
@@ -80,6 +83,14 @@ __device__ __forceinline__ void store4(OT *row, int n, int N, const float *v) {
     for (int i = 0; i < 4; ++i)
       if (n + i < N) row[n + i] = o[i];
   }
+}
+
+// g / (1 + e^-g) u with the hardware's 2^x and 1 / x (a step of float32 each):
+// with a correctly rounded division the epilogue was a third of the tiled
+// kernel's vector instructions.
+__device__ __forceinline__ float silu_mul(float g, float u) {
+  const float e = __builtin_amdgcn_exp2f(-1.44269504088896340736f * g);
+  return g * __builtin_amdgcn_rcpf(1.f + e) * u;
 }
 
 // s_waitcnt operand that waits for all but the n newest vector loads.
@@ -261,7 +272,7 @@ __global__ __launch_bounds__(kSThreads) void k_fp8_stream(Fp8GemmArgs a) {
       if (m < hi && n < a.N) {
         float o[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) o[c] = SILU ? silu_f32(v[0][c]) * v[HV - 1][c] : v[0][c];
+        for (int c = 0; c < 4; ++c) o[c] = SILU ? silu_mul(v[0][c], v[HV - 1][c]) : v[0][c];
         store4<OT>(static_cast<OT *>(a.out) + (size_t)m * a.N, n, a.N, o);
       }
     }
@@ -518,7 +529,7 @@ __global__ __launch_bounds__(kGThreads, sizeof(OT) == 2 && WT * TT <= 8 ? 3 : 2)
       if (n >= a.N) continue;
       float o[4];
 #pragma unroll
-      for (int v = 0; v < 4; ++v) o[v] = SILU ? silu_f32(acc[i][t][v]) * acc[(i + WH) % WT][t][v] : acc[i][t][v];
+      for (int v = 0; v < 4; ++v) o[v] = SILU ? silu_mul(acc[i][t][v], acc[(i + WH) % WT][t][v]) : acc[i][t][v];
       store4<OT>(row, n, a.N, o);
     }
   }
