@@ -376,7 +376,7 @@ __global__ __launch_bounds__(kGThreads, sizeof(OT) == 2 && WT * TT <= 8 ? 3 : 2)
   // load plans: a wave instruction fills 8 LDS rows (1 KB), lane i bringing
   // the chunk that lds_off places at byte 16 i of the group.  The wave's 64
   // weight rows are WC of each half.
-  uint32_t woff[8];
+  uint32_t woff[16];
 #pragma unroll
   for (int j = 0; j < WC / 8; ++j) {
     const int r = 8 * j + (lane >> 3);
@@ -449,7 +449,7 @@ __global__ __launch_bounds__(kGThreads, sizeof(OT) == 2 && WT * TT <= 8 ? 3 : 2)
   // b + 1 (XL + 1 loads, top of slab b), weights of b + 2 (2 WT loads, middle of
   // slab b); nothing moves across the barrier or the waits.
   auto step = [&](int b, const Weights &w, Weights &wn) {
-    __builtin_amdgcn_s_waitcnt(0x0f70 | (2 * WT));  // tokens of b landed; weights of b + 1 may not have
+    __builtin_amdgcn_s_waitcnt(wait_vmcnt(2 * WT));  // tokens of b landed; weights of b + 1 may not have
     __builtin_amdgcn_s_barrier();            // ... for every wave, and slab b - 1 is read out
     if (b % kWave == 0) {
 #pragma unroll
@@ -491,7 +491,7 @@ __global__ __launch_bounds__(kGThreads, sizeof(OT) == 2 && WT * TT <= 8 ? 3 : 2)
       for (int h = 0; h < HV; ++h) s[h] = sxt * sw[h];
       __builtin_amdgcn_sched_barrier(0);
       if (t == TT / 2 - 1) {
-        __builtin_amdgcn_s_waitcnt(0x0f70 | (XL + 1));  // weights of b + 1 landed
+        __builtin_amdgcn_s_waitcnt(wait_vmcnt(XL + 1));  // weights of b + 1 landed
         read_w(wn);
       }
       if (t == TT / 2) {
