@@ -296,12 +296,13 @@ __device__ __forceinline__ void store_n(DT *p, const float *f) {
   else *reinterpret_cast<V *>(p) = __builtin_bit_cast(V, a);
 }
 
-// out[t] = sum_j w[t][j] ys[pos(t, j)], ascending j; the loads of four rows
+// out[t] = sum_j w[t][j] ys[pos(t, j)], ascending j; the loads of eight rows
 // are issued together.
 template <typename DT, int N, bool WEIGHTED>
 __global__ __launch_bounds__(kThreads) void k_combine_order(
     OrderShape s, int chunks, int tpt_shift, const DT *__restrict__ ys,
     const int *__restrict__ row_pos, const float *__restrict__ w, DT *__restrict__ out) {
+  typedef typename Raw<sizeof(DT) * N>::type V;
   const int tpt = 1 << tpt_shift;
   const int t = blockIdx.x * (kThreads >> tpt_shift) + (threadIdx.x >> tpt_shift);
   const int c = blockIdx.y * tpt + (threadIdx.x & (tpt - 1));
@@ -311,22 +312,29 @@ __global__ __launch_bounds__(kThreads) void k_combine_order(
   for (int i = 0; i < N; ++i) acc[i] = 0.f;
   const int k = s.k;
   const size_t r0 = (size_t)t * k;
-  constexpr int kBatch = 4;
+  constexpr int kBatch = 8;
   for (int j0 = 0; j0 < k; j0 += kBatch) {
-    float v[kBatch][N], g[kBatch];
-    bool ok[kBatch];
+    V v[kBatch];
+    float g[kBatch];
+    int p[kBatch];
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      const int p = j0 + b < k ? row_pos[r0 + j0 + b] : -1;
-      ok[b] = (unsigned)p < (unsigned)s.R;
-      g[b] = WEIGHTED && ok[b] ? w[r0 + j0 + b] : 1.f;
-      if (ok[b]) load_n<DT, N, true>(ys + ((size_t)p * chunks + c) * N, v[b]);
+      p[b] = j0 + b < k ? row_pos[r0 + j0 + b] : -1;
+      g[b] = WEIGHTED && j0 + b < k ? w[r0 + j0 + b] : 1.f;
     }
 #pragma unroll
     for (int b = 0; b < kBatch; ++b)
-      if (ok[b]) {
+      if ((unsigned)p[b] < (unsigned)s.R)
+        v[b] = __builtin_nontemporal_load(reinterpret_cast<const V *>(ys + ((size_t)p[b] * chunks + c) * N));
 #pragma unroll
-        for (int i = 0; i < N; ++i) acc[i] = WEIGHTED ? fmaf(g[b], v[b][i], acc[i]) : acc[i] + v[b][i];
+    for (int b = 0; b < kBatch; ++b)
+      if ((unsigned)p[b] < (unsigned)s.R) {
+        const Pack<DT, N> y = __builtin_bit_cast(Pack<DT, N>, v[b]);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const float f = Elem<DT>::to_f32(y.v[i]);
+          acc[i] = WEIGHTED ? fmaf(g[b], f, acc[i]) : acc[i] + f;
+        }
       }
   }
   store_n<DT, N>(out + ((size_t)t * chunks + c) * N, acc);
