@@ -244,7 +244,7 @@ MOELORA_API moelora_status moelora_forward_noalloc(moelora_plan_t plan, int32_t 
  *                       are left as they were.  NULL (x may be NULL
  *                       too): the order only.
  * workspace: moelora_dispatch_workspace bytes (0 for small batches, at
- * most 1024 E), no initialisation.  n_tokens = 0 writes expert_start
+ * most 1024 E), no initialisation; calls that overlap need one each.  n_tokens = 0 writes expert_start
  * (zeros) and reads nothing. */
 MOELORA_API moelora_status moelora_dispatch_workspace(int32_t n_tokens, int32_t n_experts,
                                int32_t top_k, size_t *workspace_bytes);

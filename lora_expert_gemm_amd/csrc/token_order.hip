@@ -249,6 +249,8 @@ RowGrid row_grid(int T, int chunks) {
     if ((chunks + n - 1) / n * n <= (chunks + b - 1) / b * b) best = sh;
   }
   while (best > 0 && (1 << (best - 1)) >= chunks) --best;
+  // (a launch holds fewer than 2^32 threads along x)
+  while (((long long)T << best) > 0xffffff00ll - kThreads) --best;
   RowGrid g;
   g.tpt_shift = best;
   g.tiles = (chunks + (1 << best) - 1) >> best;

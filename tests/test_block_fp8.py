@@ -267,8 +267,11 @@ COUNTS = {
     "wide": [25, 40, 0, 64, 65, 7],
     "many": [130, 0, 300, 127, 1, 257],
     "hundreds": [3] * 300,
+    "onehot": [0] * 30 + [150, 0],                 # mean of 4 rows, one expert with all of them
+    "thousand": [9, 0, 17, 3, 30, 1, 8, 12] * 128,  # 1024 experts, the limit
 }
-SHAPES = [(1, 1), (16, 128), (33, 100), (130, 300), (576, 1100), (771, 130), (512, 2880)]
+SHAPES = [(1, 1), (16, 128), (33, 100), (130, 300), (576, 1100), (771, 130), (512, 2880),
+          (40, 8300)]     # more than 64 blocks
 
 
 @pytest.mark.parametrize("silu", [False, True])
@@ -292,6 +295,53 @@ def test_product(counts, N, K, silu):
             lib.moelora_fp8_gemm(R, N, K, 1, out_dtype, lib.FP8_SILU_MUL if silu else 0, x, xs[:, :R]
                                  .contiguous(), None, w, ws, o2)
             check(o2, ref, err, R)
+
+
+@pytest.mark.parametrize("counts", [[5, 0, 9], [70, 0, 200], [900, 800, 0]])
+@pytest.mark.parametrize("silu", [False, True])
+def test_ranges_that_start_late(counts, silu):
+    """Rows before the first expert's and behind the last one's belong to
+    nobody: not read, left as they were."""
+    N, K, before, behind = 160, 260, 3, 7
+    R = sum(counts)
+    for out_dtype in (lib.F32, lib.BF16):
+        x, xs, w, ws, start = make(counts, N, K, 2 if silu else 1, 5, before + behind)
+        x[:before], x[before + R:] = 0x7f, 0x7f
+        out = torch.full((before + R + behind, N), -7.0, dtype=DT[out_dtype], device="cuda")
+        lib.moelora_fp8_gemm(before + R + behind, N, K, len(counts), out_dtype,
+                             lib.FP8_SILU_MUL if silu else 0, x, xs, start + before, w, ws, out)
+        ref, err = product64(x[before:], xs[:, before:], w, ws, counts, N, K, silu, out_dtype)
+        check(out[before:], ref, err, R)
+        assert bool((out[:before] == -7).all()) and bool((out[before + R:] == -7).all())
+
+
+def test_dense_sizes_on_both_sides_of_every_choice():
+    """One expert, rows and columns around the borders where another kernel or
+    tile takes over."""
+    K = 384
+    for out_dtype in (lib.F32, lib.BF16):
+        for silu in (False, True):
+            for R, N in ((16, 200), (17, 200), (32, 200), (33, 200), (97, 9000), (128, 9000),
+                         (129, 20000), (260, 20000), (1030, 9000)):
+                x, xs, w, ws, _ = make([R], N, K, 2 if silu else 1, R + N)
+                out = torch.full((R, N), -7.0, dtype=DT[out_dtype], device="cuda")
+                lib.moelora_fp8_gemm(R, N, K, 1, out_dtype, lib.FP8_SILU_MUL if silu else 0, x, xs, None,
+                                     w, ws, out)
+                ref, err = product64(x, xs, w, ws, [R], N, K, silu, out_dtype)
+                check(out, ref, err, R)
+
+
+def test_nothing_to_gather():
+    """A shard without rows: every index points past the source."""
+    codes = torch.full((6, 128), 0xAA, dtype=torch.uint8, device="cuda")
+    scales = torch.full((1, 6), -1.0, device="cuda")
+    idx = torch.full((6,), 6, dtype=torch.int32, device="cuda")
+    lib.moelora_quantize_rows(6, 100, lib.BF16, None, 0, idx, 2, codes, scales)
+    out = torch.full((6, 32), -7.0, device="cuda")
+    w, ws = torch.zeros(3, 32, 128, dtype=torch.uint8, device="cuda"), torch.ones(3, 1, 1, device="cuda")
+    lib.moelora_fp8_gemm(6, 32, 100, 3, lib.F32, 0, codes, scales,
+                         torch.zeros(4, dtype=torch.int32, device="cuda"), w, ws, out)
+    assert bool((codes == 0xAA).all()) and bool((scales == -1).all()) and bool((out == -7).all())
 
 
 def test_every_code():

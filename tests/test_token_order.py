@@ -228,6 +228,41 @@ def test_nan_and_inf_pass_through():
     assert bad.sum() == 2 and bool(bad[3, 5]) and bool(bad[7, 11])
 
 
+def test_most_rows():
+    """R = 2^24, the limit: against numpy's stable sort."""
+    T, k, E = 1 << 19, 32, 1024
+    ids = np.random.default_rng(12).integers(-1, E, (T, k)).astype(np.int32)
+    start, rows, pos, _ = dispatch(ids, E)
+    flat = ids.reshape(-1)
+    key = np.where(flat >= 0, flat, E)
+    want = np.argsort(key, kind="stable").astype(np.int32)
+    kept = int((flat >= 0).sum())
+    assert np.array_equal(start.cpu().numpy(), np.searchsorted(key[want], np.arange(E + 1)))
+    got = rows.cpu().numpy()
+    assert np.array_equal(got[:kept], want[:kept]) and (got[kept:] == T * k).all()
+    back = pos.cpu().numpy().reshape(-1)
+    assert np.array_equal(back[want[:kept]], np.arange(kept)) and (back[flat < 0] == -1).all()
+
+
+@pytest.mark.parametrize("dtype", [lib.F32, lib.BF16])
+@pytest.mark.parametrize("T,H", [(3, 65536), (2, 65535), (1 << 24, 4)])
+def test_widest_and_longest(T, H, dtype):
+    """The limits of the width (whole chunks and odd) and of the tokens: the
+    copy, then the sum of one pick, give x back."""
+    E = 3
+    ids = np.random.default_rng(T % 97).integers(0, E, (T, 1)).astype(np.int32)
+    x = torch.randn(T, H, device="cuda").to(DT[dtype])
+    start, rows, pos, xs = dispatch(ids, E, x, dtype)
+    out = torch.zeros_like(x)
+    lib.moelora_dispatch_backward(T, H, 1, dtype, xs, pos, out)
+    assert torch.equal(out, x)
+    dys, dw = torch.zeros_like(x), torch.zeros(T, 1, device="cuda")
+    lib.moelora_combine_backward(T, H, 1, dtype, x, xs, pos, torch.ones(T, 1, device="cuda"), dys, dw)
+    assert torch.equal(dys, xs)
+    mag = (x.double() ** 2).sum(1, keepdim=True)
+    assert bool(((dw.double() - mag).abs() <= (H + 1) * U * mag).all())
+
+
 def test_rows_past_32_bit_offsets():
     """R H past 2^32 elements: the last rows are found and written."""
     T, H, E, k = 140_000, 8192, 4, 4
