@@ -70,14 +70,19 @@ def _code_only(text):
     return re.sub(r"\s+", "", text)
 
 
+# csrc files that no kernel of the layer is compiled from: the host ABI file
+# and the stand-alone operators
+NOT_LAYER_KERNELS = ("api.hip", "ops_api.hip", "ops.h", "token_order.hip", "block_fp8.hip",
+                     "fp8_gemm.hip")
+
+
 def kernel_source_hash(csrc=None):
-    """Hash of the device-kernel code (everything in csrc but the host ABI
-    file, comments and whitespace ignored), used to tell whether committed
-    counters still apply."""
+    """Hash of the layer's device-kernel code (comments and whitespace
+    ignored), used to tell whether committed counters still apply."""
     h = hashlib.sha256()
     csrc = csrc or os.path.join(ROOT, "lora_expert_gemm_amd", "csrc")
     for n in sorted(os.listdir(csrc)):
-        if n == "api.hip":
+        if n in NOT_LAYER_KERNELS:
             continue
         with open(os.path.join(csrc, n)) as f:
             h.update(n.encode() + _code_only(f.read()).encode())

@@ -32,7 +32,9 @@ constexpr int kWaves = kThreads / kWave;
 constexpr int kMaxE = 1024;
 // Up to this many routed rows one launch orders and copies: the workgroup of
 // a row finds the row's place by counting (R comparisons), so that a decode
-// step pays one launch.
+// step pays one launch.  us for 2880 bf16 columns on 32 experts, one launch
+// against three: 64 rows 2.6 / 7.2, 1024 4.1 / 8.3, 2048 6.6 / 9.3, 4096
+// 16.1 / 10.9.
 constexpr int kFusedRows = 2048;
 
 template <int BYTES> struct Raw;
