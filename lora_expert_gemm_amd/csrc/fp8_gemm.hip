@@ -120,7 +120,7 @@ __device__ __forceinline__ int lds_off(int row, int c) {
   return row * 128 + ((c ^ ((row >> 1) & 7)) << 4);
 }
 
-template <int NT, int TG, int S, bool SILU, typename OT>
+template <int NT, int TG, int S, bool ONCE, bool SILU, typename OT>
 __global__ __launch_bounds__(kSThreads) void k_fp8_stream(Fp8GemmArgs a) {
   constexpr int HV = SILU ? 2 : 1, A = HV * NT;
   constexpr int SLOT = A * 16 * 128;
@@ -195,7 +195,7 @@ __global__ __launch_bounds__(kSThreads) void k_fp8_stream(Fp8GemmArgs a) {
         for (int j = 0; j < 2 * NT; ++j)
           __builtin_amdgcn_raw_ptr_buffer_load_lds(
               res, (__attribute__((address_space(3))) void *)(ring + u * SLOT + (h * NT * 16 + 8 * j) * 128),
-              16, woff[j], b * 128, 0, kCpolNonTemporal);
+              16, woff[j], b * 128, 0, ONCE ? kCpolNonTemporal : 0);
       }
       const int bc = min(b, KB - 1);
 #pragma unroll
@@ -348,7 +348,7 @@ __device__ __forceinline__ RowTile find_tile(const Fp8GemmArgs &a, int BM, int n
   return {e, lo + r % nb * BM, hi, r / nb};
 }
 
-template <int WT, int TT, bool SILU, typename OT>
+template <int WT, int TT, bool ONCE, bool SILU, typename OT>
 __global__ __launch_bounds__(kGThreads, sizeof(OT) == 2 && WT * TT <= 8 ? 3 : 2) void k_fp8_tiled(Fp8GemmArgs a, int ncols) {
   extern __shared__ __align__(16) unsigned char smem[];
   constexpr int HV = SILU ? 2 : 1, WC = 16 * WT / HV, COLS = kGWaves * WC;  // columns a wave, a workgroup
@@ -398,7 +398,7 @@ __global__ __launch_bounds__(kGThreads, sizeof(OT) == 2 && WT * TT <= 8 ? 3 : 2)
       const __amdgpu_buffer_rsrc_t res = resource(wbase[j * 8 / WC], (int)(cols * P), b);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
           res, (__attribute__((address_space(3))) void *)(wst + 8 * j * 128), 16, woff[j % (WC / 8)],
-          b * 128, 0, 0);
+          b * 128, 0, ONCE ? kCpolNonTemporal : 0);
     }
   };
   auto read_w = [&](Weights &w) {
@@ -535,10 +535,10 @@ __global__ __launch_bounds__(kGThreads, sizeof(OT) == 2 && WT * TT <= 8 ? 3 : 2)
   }
 }
 
-template <int NT, int TG, int S, bool SILU, typename OT>
+template <int NT, int TG, int S, bool ONCE, bool SILU, typename OT>
 hipError_t stream_t(const Fp8GemmArgs &a, hipStream_t st) {
   constexpr int LDS = kSWaves * S * NT * (SILU ? 2 : 1) * 16 * 128;
-  auto kern = k_fp8_stream<NT, TG, S, SILU, OT>;
+  auto kern = k_fp8_stream<NT, TG, S, ONCE, SILU, OT>;
   hipError_t err = hipFuncSetAttribute(reinterpret_cast<const void *>(kern),
                                        hipFuncAttributeMaxDynamicSharedMemorySize, LDS);
   if (err != hipSuccess) return err;
@@ -546,11 +546,11 @@ hipError_t stream_t(const Fp8GemmArgs &a, hipStream_t st) {
                        dim3(kSThreads), LDS, st, a);
 }
 
-template <int WT, int TT, bool SILU, typename OT>
+template <int WT, int TT, bool ONCE, bool SILU, typename OT>
 hipError_t tiled_t(const Fp8GemmArgs &a, hipStream_t st) {
   constexpr int COLS = kGWaves * 16 * WT / (SILU ? 2 : 1), GM = 16 * TT;
   constexpr int LDS = kGSlots * (GM * 128 + 512) + kGWaves * 16 * WT * 128;
-  auto kern = k_fp8_tiled<WT, TT, SILU, OT>;
+  auto kern = k_fp8_tiled<WT, TT, ONCE, SILU, OT>;
   hipError_t err = hipFuncSetAttribute(reinterpret_cast<const void *>(kern),
                                        hipFuncAttributeMaxDynamicSharedMemorySize, LDS);
   if (err != hipSuccess) return err;
@@ -591,21 +591,32 @@ hipError_t gemm_t(const Fp8GemmArgs &a, hipStream_t st) {
   return FORCE;
 #endif
   constexpr int NT = SILU ? 1 : 2;  // 32 weight rows a workgroup either way
-  // (several experts: some have twice the mean, and pass their weights twice)
-  if (mean <= (a.E == 1 ? 16 : 7)) return stream_t<NT, 1, 2, SILU, OT>(a, st);
-  if (a.E == 1 && mean <= 32) return stream_t<NT, 2, 2, SILU, OT>(a, st);
+  // (several experts: some have twice the mean, and pass their weights twice.
+  // One expert's weights may still lie in the last-level cache, several are
+  // streamed past it: a single row of 4096 -> 11008 9.9 us against 10.6, the
+  // 16-token decode 59 us against 66)
+  if (a.E > 1 && mean <= 7) return stream_t<NT, 1, 2, true, SILU, OT>(a, st);
+  if (a.E == 1 && mean <= 16) return stream_t<NT, 1, 2, false, SILU, OT>(a, st);
+  if (a.E == 1 && mean <= 32) return stream_t<NT, 2, 2, false, SILU, OT>(a, st);
   if constexpr (sizeof(OT) == 2) {
-    if (mean >= 56 && tiled_wgs(a, SILU, 4, 8) >= 512) return tiled_t<4, 8, SILU, OT>(a, st);
-    if (mean >= 96 && tiled_wgs(a, SILU, 2, 8) >= 512) return tiled_t<2, 8, SILU, OT>(a, st);
+    if (mean >= 56 && tiled_wgs(a, SILU, 4, 8) >= 512) return tiled_t<4, 8, false, SILU, OT>(a, st);
+    if (mean >= 96 && tiled_wgs(a, SILU, 2, 8) >= 512) return tiled_t<2, 8, false, SILU, OT>(a, st);
   } else {
     // float32 results: widened operands leave registers for 64 tokens (the
     // 25600-row gate_up 866 us against 919 with 2x4, g1024 201 against 198)
-    if (mean >= 192 && tiled_wgs(a, SILU, 4, 4) >= 512) return tiled_t<4, 4, SILU, OT>(a, st);
+    if (mean >= 192 && tiled_wgs(a, SILU, 4, 4) >= 512) return tiled_t<4, 4, false, SILU, OT>(a, st);
   }
+  // Where an expert's rows mostly fit one row tile its weights are read once:
+  // past the caches then (16-row experts of 128: 78 -> 70 us, g64 94 -> 83,
+  // g256 109 -> 105; with seven row tiles an expert, 471 -> 535).  Not for one
+  // expert, whose weights may still lie in the last-level cache (d64 18 -> 24).
   // (float32, 128 experts of 21 rows, 2050 -> 771: 2x2 56 us, 2x4 61)
-  if (tiled_wgs(a, SILU, 2, 4) >= 160 && (sizeof(OT) == 2 || mean > 24))
-    return tiled_t<2, 4, SILU, OT>(a, st);
-  return tiled_t<2, 2, SILU, OT>(a, st);
+  if (tiled_wgs(a, SILU, 2, 4) >= 160 && (sizeof(OT) == 2 || mean > 24)) {
+    if (a.E > 1 && mean <= 40) return tiled_t<2, 4, true, SILU, OT>(a, st);
+    return tiled_t<2, 4, false, SILU, OT>(a, st);
+  }
+  if (a.E > 1 && mean <= 24) return tiled_t<2, 2, true, SILU, OT>(a, st);
+  return tiled_t<2, 2, false, SILU, OT>(a, st);
 }
 
 // Every kernel gemm_t can pick (launch sites that only look kernels up).
@@ -614,14 +625,16 @@ hipError_t resolve_t() {
   constexpr int NT = SILU ? 1 : 2;
   Fp8GemmArgs a{};
   a.R = a.N = a.K = a.E = a.KB = a.NB = 1, a.P = 128;
-  hipError_t e[6] = {stream_t<NT, 1, 2, SILU, OT>(a, nullptr), stream_t<NT, 2, 2, SILU, OT>(a, nullptr),
-                     tiled_t<2, 2, SILU, OT>(a, nullptr), tiled_t<2, 4, SILU, OT>(a, nullptr)};
+  hipError_t e[9] = {stream_t<NT, 1, 2, true, SILU, OT>(a, nullptr),  stream_t<NT, 1, 2, false, SILU, OT>(a, nullptr),
+                     stream_t<NT, 2, 2, false, SILU, OT>(a, nullptr),
+                     tiled_t<2, 2, false, SILU, OT>(a, nullptr),     tiled_t<2, 2, true, SILU, OT>(a, nullptr),
+                     tiled_t<2, 4, false, SILU, OT>(a, nullptr),     tiled_t<2, 4, true, SILU, OT>(a, nullptr)};
   if constexpr (sizeof(OT) == 2) {
-    e[4] = tiled_t<2, 8, SILU, OT>(a, nullptr);
-    e[5] = tiled_t<4, 8, SILU, OT>(a, nullptr);
+    e[7] = tiled_t<2, 8, false, SILU, OT>(a, nullptr);
+    e[8] = tiled_t<4, 8, false, SILU, OT>(a, nullptr);
   } else {
-    e[4] = tiled_t<4, 4, SILU, OT>(a, nullptr);
-    e[5] = hipSuccess;
+    e[7] = tiled_t<4, 4, false, SILU, OT>(a, nullptr);
+    e[8] = hipSuccess;
   }
   for (hipError_t r : e)
     if (r != hipSuccess) return r;
