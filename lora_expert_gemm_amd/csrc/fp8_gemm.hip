@@ -110,7 +110,11 @@ __device__ __forceinline__ int row_bound(const int *start, int e, int R) {
 // an LDS ring of its own, S blocks deep, in whole 128-byte lines (8 lanes a
 // line): loaded straight into operand registers, 16 rows at 64 bytes an
 // instruction, the address unit and not HBM set the pace.  Tokens, few and
-// shared by all workgroups, come from cache into registers.
+// shared by all workgroups, come from cache into registers.  Bound by the
+// weights' bytes: the 16-token decode step of 32 experts (392 MB of 23 experts
+// hit) takes 56-59 us, 6.6 TB/s (77 us with the weights straight into
+// registers; 75 us with a ring of 4 blocks, whose 64 KB leave two workgroups
+// on a CU where 2 blocks leave four), one row of 4096 -> 11008 (45 MB) 9.8 us.
 constexpr int kSWaves = 4;
 constexpr int kSThreads = kSWaves * kWave;
 
@@ -282,19 +286,33 @@ __global__ __launch_bounds__(kSThreads) void k_fp8_stream(Fp8GemmArgs a) {
 
 // --------------------------------------------------------------- many rows
 //
-// 16 TT rows x 256 weight rows (SILU: 128 gate + the matching 128 up) a
-// workgroup of 4 waves, two workgroups per CU.  A wave owns 64 weight rows
-// and all 16 TT tokens, so no other wave reads its weights: they go straight
-// into its registers, one slab (a block of 128) ahead, and LDS holds only
-// what the waves share, the token rows and their scales, two slabs ahead in
-// three stages.  (Weights through LDS too, 128 x 512 tiles of 8 waves: 672 us
-// for the 25600-row gate_up product, of which ~190 us were the extra LDS
-// fills and 140 us the fragment reads.)  A token row contributes one 128-byte
-// line a slab, fetched by 8 lanes; its 16-byte chunk c sits at chunk
-// c ^ ((row / 2) % 8) of the LDS row, so the 16 rows that 16 lanes read at
-// one chunk fall on 16 distinct bank groups.  Rows past the expert's last,
-// and weight rows past N, lie past their buffer resource's end: their loads
-// fetch nothing, and their outputs are dropped.
+// 16 TT token rows x 64 WT weight rows (SILU: half gate, half up) a workgroup
+// of 4 waves, two workgroups or more per CU.  A wave owns 16 WT weight rows
+// against all the tokens.  Everything arrives in slabs of one block of 128,
+// one 128-byte line a row, fetched by 8 lanes straight into LDS: the tokens
+// and their scales into two stages that the waves share (loaded one slab
+// ahead, one barrier a slab), the weights, which no other wave reads, into a
+// place of the wave's own, from which they go on to registers half a slab
+// before they are needed, so that the next slab's can be on their way with no
+// barrier.  A row's 16-byte chunk c sits at chunk c ^ ((row / 2) % 8) of its
+// LDS row, so the 16 rows that 16 lanes read at one chunk fall on 16 distinct
+// bank groups.  Rows past the expert's last, and weight rows past N, lie past
+// their buffer resource's end: their loads fetch nothing, and their outputs
+// are dropped.
+//
+// What led here, for the 25600-row gate_up product of 32 experts (849 GFLOP;
+// the same card's library product of plain E4M3 without block scales runs at
+// 2.6-2.75 PFLOP/s): 128 x 512 tiles of 8 waves, everything through two shared
+// stages, 672 us; weights straight into registers, two 4-wave workgroups per
+// CU, 574 us (the address unit takes 16 rows at 64 bytes an instruction);
+// weights through the wave's own LDS in whole lines, 523 us where the step
+// before took 671 (another box); block sums scaled four MFMAs after they were
+// formed, 484 us; the shorter epilogue, 452-474 us by box: 1.8-1.9 PFLOP/s.
+// The matrix cores are busy 53 % of the cycles, at 1.8 GHz under the card's
+// power limit.  Without its loads the loop keeps them 68 % busy, and leaving
+// out the waits for the loads changes nothing: the loads' own passage
+// (1.3 GB from beyond L2, 77 % L2 hits) and the one multiply-add an
+// accumulator and block that the scales cost bound it now.
 constexpr int kGWaves = 4, kGThreads = kGWaves * kWave;
 constexpr int kGSlots = 2;              // stages of tokens
 
@@ -349,10 +367,11 @@ __device__ __forceinline__ RowTile find_tile(const Fp8GemmArgs &a, int BM, int n
 }
 
 template <int WT, int TT, bool ONCE, bool SILU, typename OT>
-__global__ __launch_bounds__(kGThreads, sizeof(OT) == 2 && WT * TT <= 8 ? 3 : 2) void k_fp8_tiled(Fp8GemmArgs a, int ncols) {
+__global__ __launch_bounds__(kGThreads, sizeof(OT) == 2 && WT * TT <= 8 ? 3 : 2) void k_fp8_tiled(
+    Fp8GemmArgs a, int ncols) {
   extern __shared__ __align__(16) unsigned char smem[];
-  constexpr int HV = SILU ? 2 : 1, WC = 16 * WT / HV, COLS = kGWaves * WC;  // columns a wave, a workgroup
-  constexpr int WH = WT / HV;           // weight tiles of a half
+  constexpr int HV = SILU ? 2 : 1, WH = WT / HV;        // weight tiles of a half
+  constexpr int WC = 16 * WH, COLS = kGWaves * WC;      // columns a wave, a workgroup
   constexpr int GM = 16 * TT, STAGE = GM * 128 + 512;
   constexpr int XL = GM / 8 / kGWaves;  // token loads a wave and slab
   typedef Block<sizeof(OT) == 4> B;
@@ -449,8 +468,9 @@ __global__ __launch_bounds__(kGThreads, sizeof(OT) == 2 && WT * TT <= 8 ? 3 : 2)
   // b + 1 (XL + 1 loads, top of slab b), weights of b + 2 (2 WT loads, middle of
   // slab b); nothing moves across the barrier or the waits.
   auto step = [&](int b, const Weights &w, Weights &wn) {
-    __builtin_amdgcn_s_waitcnt(wait_vmcnt(2 * WT));  // tokens of b landed; weights of b + 1 may not have
-    __builtin_amdgcn_s_barrier();            // ... for every wave, and slab b - 1 is read out
+    // tokens of b landed (weights of b + 1 may not have) ...
+    __builtin_amdgcn_s_waitcnt(wait_vmcnt(2 * WT));
+    __builtin_amdgcn_s_barrier();  // ... for every wave, and slab b - 1 is read out
     if (b % kWave == 0) {
 #pragma unroll
       for (int h = 0; h < HV; ++h) ws[h] = wsp[(size_t)h * a.NB * KB + min(b + lane, KB - 1)];
@@ -572,7 +592,7 @@ long long tiled_wgs(const Fp8GemmArgs &a, bool silu, int WT, int TT) {
 // tile leaves (two of 128 tokens x 256 weight rows fit a CU: 512 on the
 // chip).  us on one box, E = 32, top-4, 2880 -> 2 x 2880 with SILU ("g", by
 // tokens), and dense 4096 -> 11008 ("d", by rows):
-//            few rows      tiles: weight tiles of a wave x token tiles
+//            few rows      tiles: WT x TT, weights through the caches
 //            1x16  2x16    2x2   2x4   2x8   4x8
 //   g32      73    81      87    89    89   106
 //   g64      97    93      97    94    97   110
@@ -587,9 +607,6 @@ long long tiled_wgs(const Fp8GemmArgs &a, bool silu, int WT, int TT) {
 template <bool SILU, typename OT>
 hipError_t gemm_t(const Fp8GemmArgs &a, hipStream_t st) {
   const int mean = a.R / (a.E < a.R ? a.E : a.R);  // rows an expert, if all are hit
-#ifdef FORCE
-  return FORCE;
-#endif
   constexpr int NT = SILU ? 1 : 2;  // 32 weight rows a workgroup either way
   // (several experts: some have twice the mean, and pass their weights twice.
   // One expert's weights may still lie in the last-level cache, several are
