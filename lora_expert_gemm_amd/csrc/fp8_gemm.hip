@@ -393,8 +393,8 @@ __global__ __launch_bounds__(kGThreads, sizeof(OT) == 2 && WT * TT <= 8 ? 3 : 2)
                                              kBufferWord3);
   };
   // load plans: a wave instruction fills 8 LDS rows (1 KB), lane i bringing
-  // the chunk that lds_off places at byte 16 i of the group.  The wave's 64
-  // weight rows are WC of each half.
+  // the chunk that lds_off places at byte 16 i of the group.  The wave's
+  // 16 WT weight rows are WC of each half.
   uint32_t woff[16];
 #pragma unroll
   for (int j = 0; j < WC / 8; ++j) {
@@ -441,7 +441,7 @@ __global__ __launch_bounds__(kGThreads, sizeof(OT) == 2 && WT * TT <= 8 ? 3 : 2)
         256 * (wave & 1) + 4 * lane, 0, 0, 0);
   };
   // scales of the wave's weight block: 64 slabs at a time, one a lane (the
-  // wave's 64, or 32 + 32, weight rows lie in one block of 128)
+  // wave's WC columns lie in one block of 128)
   const float *wsp = a.ws + (mat * a.NB + min((n0 + WC * wave) / 128, a.NB - 1)) * KB;
   float ws[HV];
 
@@ -468,9 +468,10 @@ __global__ __launch_bounds__(kGThreads, sizeof(OT) == 2 && WT * TT <= 8 ? 3 : 2)
   // b + 1 (XL + 1 loads, top of slab b), weights of b + 2 (2 WT loads, middle of
   // slab b); nothing moves across the barrier or the waits.
   auto step = [&](int b, const Weights &w, Weights &wn) {
-    // tokens of b landed (weights of b + 1 may not have) ...
-    __builtin_amdgcn_s_waitcnt(wait_vmcnt(2 * WT));
-    __builtin_amdgcn_s_barrier();  // ... for every wave, and slab b - 1 is read out
+    // tokens of b landed (weights of b + 1 may not have) and this wave's reads
+    // of slab b - 1 done (lgkmcnt(0)) ...
+    __builtin_amdgcn_s_waitcnt(wait_vmcnt(2 * WT) & ~0x0f00);
+    __builtin_amdgcn_s_barrier();  // ... for every wave
     if (b % kWave == 0) {
 #pragma unroll
       for (int h = 0; h < HV; ++h) ws[h] = wsp[(size_t)h * a.NB * KB + min(b + lane, KB - 1)];
