@@ -306,8 +306,8 @@ __global__ __launch_bounds__(kSThreads) void k_fp8_stream(Fp8GemmArgs a) {
 // stages, 672 us; weights straight into registers, two 4-wave workgroups per
 // CU, 574 us (the address unit takes 16 rows at 64 bytes an instruction);
 // weights through the wave's own LDS in whole lines, 523 us where the step
-// before took 671 (another box); block sums scaled four MFMAs after they were
-// formed, 484 us; the shorter epilogue, 452-474 us by box: 1.8-1.9 PFLOP/s.
+// before took 671 (another card); block sums scaled four MFMAs after they were
+// formed, 484 us; the shorter epilogue, 452-474 us by card: 1.8-1.9 PFLOP/s.
 // The matrix cores are busy 53 % of the cycles, at 1.8 GHz under the card's
 // power limit.  Without its loads the loop keeps them 68 % busy, and leaving
 // out the waits for the loads changes nothing: the loads' own passage
@@ -591,7 +591,7 @@ long long tiled_wgs(const Fp8GemmArgs &a, bool silu, int WT, int TT) {
 
 // Which kernel, by the mean rows of an expert and by how many workgroups a
 // tile leaves (two of 128 tokens x 256 weight rows fit a CU: 512 on the
-// chip).  us on one box, E = 32, top-4, 2880 -> 2 x 2880 with SILU ("g", by
+// chip).  us on one card, E = 32, top-4, 2880 -> 2 x 2880 with SILU ("g", by
 // tokens), and dense 4096 -> 11008 ("d", by rows):
 //            few rows      tiles: WT x TT, weights through the caches
 //            1x16  2x16    2x2   2x4   2x8   4x8
