@@ -27,7 +27,8 @@ constexpr int kLanes = 16;   // lanes on a block, 8 elements each
 constexpr int kGroups = kThreads / kLanes;
 
 // Eight elements of a row of K from element c on, zeros past K, as they are
-// stored (bf16: two a dword).
+// stored (bf16: two a dword).  Whole ones are 16-byte loads, which need no
+// more than 2-byte alignment here.
 template <typename DT> struct Raw8;
 template <> struct Raw8<uint16_t> {
   u32x4_t v;
@@ -35,21 +36,20 @@ template <> struct Raw8<uint16_t> {
 template <> struct Raw8<float> {
   u32x4_t v[2];
 };
-template <typename DT, bool VEC>
+template <typename DT>
 __device__ __forceinline__ Raw8<DT> load8(const DT *row, int c, int K) {
-  if constexpr (VEC && sizeof(DT) == 2) {
-    return {c < K ? *reinterpret_cast<const u32x4_t *>(row + c) : u32x4_t{0, 0, 0, 0}};
-  } else if constexpr (VEC) {
-    return {{c < K ? *reinterpret_cast<const u32x4_t *>(row + c) : u32x4_t{0, 0, 0, 0},
-             c + 4 < K ? *reinterpret_cast<const u32x4_t *>(row + c + 4) : u32x4_t{0, 0, 0, 0}}};
-  } else {
-    struct Eight {
-      DT e[8];
-    } f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f.e[i] = c + i < K ? row[c + i] : DT(0);
-    return __builtin_bit_cast(Raw8<DT>, f);
+  typedef u32x4_t mem __attribute__((aligned(2)));
+  const mem *p = reinterpret_cast<const mem *>(row + c);
+  if (c + 8 <= K) {
+    if constexpr (sizeof(DT) == 2) return {*p};
+    else return {{p[0], p[1]}};
   }
+  struct Eight {
+    DT e[8];
+  } f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f.e[i] = c + i < K ? row[c + i] : DT(0);
+  return __builtin_bit_cast(Raw8<DT>, f);
 }
 
 __device__ __forceinline__ void to_f32(const Raw8<uint16_t> &r, float *f) {
@@ -125,7 +125,7 @@ __device__ __forceinline__ uint2 codes8(const Raw8<DT> &r, float inv, bool odd) 
 // The blocks' loads are all issued before the first is used; the rows'
 // scales of one block are neighbours in memory.
 constexpr int kUnroll = 4;
-template <typename DT, bool VEC>
+template <typename DT>
 __global__ __launch_bounds__(kThreads) void k_quant_rows(QuantRowsArgs a, int KB, int per_wg) {
   const int g = threadIdx.x / kLanes, l = threadIdx.x % kLanes;
   const int r = blockIdx.x * kGroups + g;
@@ -143,7 +143,7 @@ __global__ __launch_bounds__(kThreads) void k_quant_rows(QuantRowsArgs a, int KB
     Raw8<DT> v[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u)
-      if (b0 + u < b_end) v[u] = load8<DT, VEC>(row, (b0 + u) * kBlk + l * 8, a.K);
+      if (b0 + u < b_end) v[u] = load8<DT>(row, (b0 + u) * kBlk + l * 8, a.K);
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       if (b0 + u >= b_end) break;
@@ -170,7 +170,7 @@ __global__ __launch_bounds__(kThreads) void k_quant_rows(QuantRowsArgs a, int KB
 // the conversion; the transposed copy goes through LDS, four rows x four
 // codes at a time.
 constexpr int kPitch = kBlk + 4;  // LDS bytes per row of codes
-template <typename DT, bool VEC>
+template <typename DT>
 __global__ __launch_bounds__(kThreads) void k_quant_weights(QuantWeightsArgs a, int NB, int KB) {
   __shared__ uint32_t wmax[kThreads / kWave];
   __shared__ __align__(16) uint8_t tile[kBlk * kPitch];
@@ -184,7 +184,7 @@ __global__ __launch_bounds__(kThreads) void k_quant_weights(QuantWeightsArgs a, 
 #pragma unroll
   for (int i = 0; i < kPass; ++i) {
     const int n = n0 + i * kGroups + g;
-    v[i] = load8<DT, VEC>(w + (size_t)min(n, a.N - 1) * a.K, k0 + l * 8, n < a.N ? a.K : 0);
+    v[i] = load8<DT>(w + (size_t)min(n, a.N - 1) * a.K, k0 + l * 8, n < a.N ? a.K : 0);
   }
   auto block_max = [&](uint32_t m) {
 #pragma unroll
@@ -251,32 +251,28 @@ __global__ __launch_bounds__(kThreads) void k_quant_weights(QuantWeightsArgs a, 
   }
 }
 
-template <typename DT, bool VEC>
+template <typename DT>
 hipError_t rows_t(const QuantRowsArgs &a, hipStream_t st) {
   const int KB = (a.K + kBlk - 1) / kBlk;
   const int groups = (a.M + kGroups - 1) / kGroups;
-  return launch_kernel(k_quant_rows<DT, VEC>, dim3(groups, (KB + kUnroll - 1) / kUnroll), dim3(kThreads),
+  return launch_kernel(k_quant_rows<DT>, dim3(groups, (KB + kUnroll - 1) / kUnroll), dim3(kThreads),
                        0, st, a, KB, kUnroll);
 }
 
-template <typename DT, bool VEC>
+template <typename DT>
 hipError_t weights_t(const QuantWeightsArgs &a, hipStream_t st) {
   const int KB = (a.K + kBlk - 1) / kBlk, NB = (a.N + kBlk - 1) / kBlk;
-  return launch_kernel(k_quant_weights<DT, VEC>, dim3(KB, NB, a.mats), dim3(kThreads), 0, st, a, NB, KB);
+  return launch_kernel(k_quant_weights<DT>, dim3(KB, NB, a.mats), dim3(kThreads), 0, st, a, NB, KB);
 }
 
 }  // namespace
 
-// VEC: rows of a multiple of 16 bytes (and so every chunk of eight elements,
-// or four, inside the row or outside it).
 hipError_t launch_quantize_rows(const QuantRowsArgs &a, bool bf16, hipStream_t st) {
-  if (bf16) return a.K % 8 == 0 ? rows_t<uint16_t, true>(a, st) : rows_t<uint16_t, false>(a, st);
-  return a.K % 4 == 0 ? rows_t<float, true>(a, st) : rows_t<float, false>(a, st);
+  return bf16 ? rows_t<uint16_t>(a, st) : rows_t<float>(a, st);
 }
 
 hipError_t launch_quantize_weights(const QuantWeightsArgs &a, bool bf16, hipStream_t st) {
-  if (bf16) return a.K % 8 == 0 ? weights_t<uint16_t, true>(a, st) : weights_t<uint16_t, false>(a, st);
-  return a.K % 4 == 0 ? weights_t<float, true>(a, st) : weights_t<float, false>(a, st);
+  return bf16 ? weights_t<uint16_t>(a, st) : weights_t<float>(a, st);
 }
 
 }  // namespace moelora

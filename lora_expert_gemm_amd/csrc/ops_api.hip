@@ -34,7 +34,7 @@ hipError_t resolve_all() {
     if (e == hipSuccess) e = r;
   };
   for (int bf16 = 0; bf16 < 2; ++bf16) {
-    for (int H : {8, 2, 1}) {
+    for (int H : {8, 1}) {  // rows of 16 bytes and more, and shorter ones
       for (int R : {1, 1 << 20}) {
         const OrderShape s{R, H, 1, 1, R, bf16 != 0};
         need(launch_dispatch(s, f, fi, fi, fi, fi, f, fi, nullptr));
@@ -42,9 +42,9 @@ hipError_t resolve_all() {
         need(launch_combine_rows(s, f, fi, nullptr, f, nullptr));
         need(launch_combine_backward(s, f, f, fi, ff, f, ff, nullptr));
       }
-      need(launch_quantize_rows(QuantRowsArgs{f, nullptr, fb, ff, 1, H, 1, 1}, bf16, nullptr));
-      need(launch_quantize_weights(QuantWeightsArgs{f, fb, nullptr, ff, nullptr, 1, 1, H}, bf16, nullptr));
     }
+    need(launch_quantize_rows(QuantRowsArgs{f, nullptr, fb, ff, 1, 1, 1, 1}, bf16, nullptr));
+    need(launch_quantize_weights(QuantWeightsArgs{f, fb, nullptr, ff, nullptr, 1, 1, 1}, bf16, nullptr));
     for (int silu = 0; silu < 2; ++silu) need(resolve_fp8_gemm(silu, bf16));
   }
   return e;

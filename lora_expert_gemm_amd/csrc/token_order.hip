@@ -37,10 +37,32 @@ constexpr int kMaxE = 1024;
 // 16.1 / 10.9.
 constexpr int kFusedRows = 2048;
 
+// What a lane moves at once, and how it lies in memory.  16-byte accesses need
+// no more than 2-byte alignment here, so rows of any length are moved 16 bytes
+// a lane: chunk c of a row starts at c steps of 16 bytes, the last one at the
+// row's end less 16 (it may cover bytes of the one before once more, with the
+// same values).  Rows shorter than 16 bytes go element by element.
 template <int BYTES> struct Raw;
-template <> struct Raw<16> { typedef u32x4_t type; };
-template <> struct Raw<4> { typedef uint32_t type; };
-template <> struct Raw<2> { typedef uint16_t type; };
+template <> struct Raw<16> {
+  typedef u32x4_t type;
+  typedef u32x4_t mem __attribute__((aligned(2)));
+};
+template <> struct Raw<4> {
+  typedef uint32_t type;
+  typedef uint32_t mem;
+};
+template <> struct Raw<2> {
+  typedef uint16_t type;
+  typedef uint16_t mem;
+};
+template <int BYTES>
+__device__ __forceinline__ const typename Raw<BYTES>::mem *raw(const void *p) {
+  return static_cast<const typename Raw<BYTES>::mem *>(p);
+}
+template <int BYTES>
+__device__ __forceinline__ typename Raw<BYTES>::mem *raw(void *p) {
+  return static_cast<typename Raw<BYTES>::mem *>(p);
+}
 
 __device__ __forceinline__ bool held(int e, int E) { return (unsigned)e < (unsigned)E; }
 
@@ -48,9 +70,9 @@ __device__ __forceinline__ bool held(int e, int E) { return (unsigned)e < (unsig
 // Workgroup R writes expert_start and the sentinel tail of sorted_rows.
 template <int BYTES>
 __global__ __launch_bounds__(kThreads) void k_dispatch_fused(
-    OrderShape s, int chunks, const typename Raw<BYTES>::type *__restrict__ x,
-    const int *__restrict__ ids, int *__restrict__ expert_start, int *__restrict__ sorted_rows,
-    int *__restrict__ row_pos, typename Raw<BYTES>::type *__restrict__ xs) {
+    OrderShape s, int row_bytes, const char *__restrict__ x, const int *__restrict__ ids,
+    int *__restrict__ expert_start, int *__restrict__ sorted_rows, int *__restrict__ row_pos,
+    char *__restrict__ xs) {
   __shared__ int part[kWaves];
   __shared__ int hist[kMaxE];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
@@ -78,9 +100,12 @@ __global__ __launch_bounds__(kThreads) void k_dispatch_fused(
       row_pos[p] = pos;
     }
     if (xs) {
-      const auto *src = x + (size_t)(p / s.k) * chunks;
-      auto *dst = xs + (size_t)pos * chunks;
-      for (int c = tid; c < chunks; c += kThreads) dst[c] = src[c];
+      const char *src = x + (size_t)(p / s.k) * row_bytes;
+      char *dst = xs + (size_t)pos * row_bytes;
+      for (int c = tid * BYTES; c < row_bytes; c += kThreads * BYTES) {
+        const int o = min(c, row_bytes - BYTES);
+        *raw<BYTES>(dst + o) = *raw<BYTES>(src + o);
+      }
     }
     return;
   }
@@ -238,8 +263,7 @@ __global__ __launch_bounds__(kThreads) void k_order_place(
   for (int q = kept + me * kThreads + tid; q < R; q += nch * kThreads) sorted_rows[q] = R;
 }
 
-// Threads a token and its tiles: one 16-byte chunk (or less, for rows that
-// are no multiple of 16 bytes) a thread, `tpt` threads side by side.
+// Threads a token and its tiles: one chunk a thread, `tpt` threads side by side.
 struct RowGrid {
   int tpt_shift, tiles;
   dim3 grid;
@@ -263,18 +287,21 @@ RowGrid row_grid(int T, int chunks) {
 
 // xs[pos(t, j)] = x[t] for every j: a token is read once.
 template <int BYTES>
-__global__ __launch_bounds__(kThreads) void k_scatter(
-    OrderShape s, int chunks, int tpt_shift, const typename Raw<BYTES>::type *__restrict__ x,
-    const int *__restrict__ row_pos, typename Raw<BYTES>::type *__restrict__ xs) {
+__global__ __launch_bounds__(kThreads) void k_scatter(OrderShape s, int row_bytes, int tpt_shift,
+                                                      const char *__restrict__ x,
+                                                      const int *__restrict__ row_pos,
+                                                      char *__restrict__ xs) {
   const int tpt = 1 << tpt_shift;
   const int t = blockIdx.x * (kThreads >> tpt_shift) + (threadIdx.x >> tpt_shift);
   const int c = blockIdx.y * tpt + (threadIdx.x & (tpt - 1));
-  if (t >= s.T || c >= chunks) return;
-  const auto v = x[(size_t)t * chunks + c];
+  if (t >= s.T || c * BYTES >= row_bytes) return;
+  const int o = min(c * BYTES, row_bytes - BYTES);
+  const typename Raw<BYTES>::type v = *raw<BYTES>(x + (size_t)t * row_bytes + o);
   const int *pos = row_pos + (size_t)t * s.k;
   for (int j = 0; j < s.k; ++j) {
     const int p = pos[j];
-    if ((unsigned)p < (unsigned)s.R) __builtin_nontemporal_store(v, &xs[(size_t)p * chunks + c]);
+    if ((unsigned)p < (unsigned)s.R)
+      __builtin_nontemporal_store(v, raw<BYTES>(xs + (size_t)p * row_bytes + o));
   }
 }
 
@@ -282,35 +309,32 @@ __global__ __launch_bounds__(kThreads) void k_scatter(
 template <typename DT, int N> struct Pack {
   DT v[N];
 };
-template <typename DT, int N, bool NT = false>
-__device__ __forceinline__ void load_n(const DT *p, float *f) {
-  typedef typename Raw<sizeof(DT) * N>::type V;
-  const V *q = reinterpret_cast<const V *>(p);
-  const Pack<DT, N> a = __builtin_bit_cast(Pack<DT, N>, NT ? __builtin_nontemporal_load(q) : *q);
+template <typename DT, int N>
+__device__ __forceinline__ void unpack(typename Raw<sizeof(DT) * N>::type v, float *f) {
+  const Pack<DT, N> a = __builtin_bit_cast(Pack<DT, N>, v);
 #pragma unroll
   for (int i = 0; i < N; ++i) f[i] = Elem<DT>::to_f32(a.v[i]);
 }
-template <typename DT, int N, bool NT = false>
-__device__ __forceinline__ void store_n(DT *p, const float *f) {
+template <typename DT, int N>
+__device__ __forceinline__ typename Raw<sizeof(DT) * N>::type pack(const float *f) {
   Pack<DT, N> a;
 #pragma unroll
   for (int i = 0; i < N; ++i) a.v[i] = Elem<DT>::from_f32(f[i]);
-  typedef typename Raw<sizeof(DT) * N>::type V;
-  if (NT) __builtin_nontemporal_store(__builtin_bit_cast(V, a), reinterpret_cast<V *>(p));
-  else *reinterpret_cast<V *>(p) = __builtin_bit_cast(V, a);
+  return __builtin_bit_cast(typename Raw<sizeof(DT) * N>::type, a);
 }
 
 // out[t] = sum_j w[t][j] ys[pos(t, j)], ascending j; the loads of eight rows
 // are issued together.
 template <typename DT, int N, bool WEIGHTED>
 __global__ __launch_bounds__(kThreads) void k_combine_order(
-    OrderShape s, int chunks, int tpt_shift, const DT *__restrict__ ys,
-    const int *__restrict__ row_pos, const float *__restrict__ w, DT *__restrict__ out) {
-  typedef typename Raw<sizeof(DT) * N>::type V;
+    OrderShape s, int tpt_shift, const DT *__restrict__ ys, const int *__restrict__ row_pos,
+    const float *__restrict__ w, DT *__restrict__ out) {
+  constexpr int BYTES = sizeof(DT) * N;
   const int tpt = 1 << tpt_shift;
   const int t = blockIdx.x * (kThreads >> tpt_shift) + (threadIdx.x >> tpt_shift);
   const int c = blockIdx.y * tpt + (threadIdx.x & (tpt - 1));
-  if (t >= s.T || c >= chunks) return;
+  if (t >= s.T || c * N >= s.H) return;
+  const int o = min(c * N, s.H - N);
   float acc[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) acc[i] = 0.f;
@@ -318,7 +342,7 @@ __global__ __launch_bounds__(kThreads) void k_combine_order(
   const size_t r0 = (size_t)t * k;
   constexpr int kBatch = 8;
   for (int j0 = 0; j0 < k; j0 += kBatch) {
-    V v[kBatch];
+    typename Raw<BYTES>::type v[kBatch];
     float g[kBatch];
     int p[kBatch];
 #pragma unroll
@@ -329,53 +353,54 @@ __global__ __launch_bounds__(kThreads) void k_combine_order(
 #pragma unroll
     for (int b = 0; b < kBatch; ++b)
       if ((unsigned)p[b] < (unsigned)s.R)
-        v[b] = __builtin_nontemporal_load(reinterpret_cast<const V *>(ys + ((size_t)p[b] * chunks + c) * N));
+        v[b] = __builtin_nontemporal_load(raw<BYTES>(ys + (size_t)p[b] * s.H + o));
 #pragma unroll
     for (int b = 0; b < kBatch; ++b)
       if ((unsigned)p[b] < (unsigned)s.R) {
-        const Pack<DT, N> y = __builtin_bit_cast(Pack<DT, N>, v[b]);
+        float f[N];
+        unpack<DT, N>(v[b], f);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const float f = Elem<DT>::to_f32(y.v[i]);
-          acc[i] = WEIGHTED ? fmaf(g[b], f, acc[i]) : acc[i] + f;
-        }
+        for (int i = 0; i < N; ++i) acc[i] = WEIGHTED ? fmaf(g[b], f[i], acc[i]) : acc[i] + f[i];
       }
   }
-  store_n<DT, N>(out + ((size_t)t * chunks + c) * N, acc);
+  *raw<BYTES>(out + (size_t)t * s.H + o) = pack<DT, N>(acc);
 }
 
 // One wave per routed row: dys[pos] = w dout[t], dw = <dout[t], ys[pos]>.
 template <typename DT, int N>
 __global__ __launch_bounds__(kThreads) void k_combine_backward(
-    OrderShape s, int chunks, const DT *__restrict__ dout, const DT *__restrict__ ys,
+    OrderShape s, const DT *__restrict__ dout, const DT *__restrict__ ys,
     const int *__restrict__ row_pos, const float *__restrict__ w, DT *__restrict__ dys,
     float *__restrict__ dw) {
+  constexpr int BYTES = sizeof(DT) * N;
   const int lane = threadIdx.x & (kWave - 1);
   const int p = __builtin_amdgcn_readfirstlane(blockIdx.x * kWaves + threadIdx.x / kWave);
   if (p >= s.R) return;
-  const int pos = row_pos[p];
+  const int pos = row_pos[p], H = s.H;
   if ((unsigned)pos >= (unsigned)s.R) {
     if (dw && lane == 0) dw[p] = 0.f;
     return;
   }
   const float g = w ? w[p] : 1.f;
-  const DT *d = dout + (size_t)(p / s.k) * chunks * N;
-  const size_t row = (size_t)pos * chunks * N;
+  const DT *d = dout + (size_t)(p / s.k) * H;
+  const size_t row = (size_t)pos * H;
   float sum = 0.f;
 #pragma unroll 2
-  for (int c = lane; c < chunks; c += kWave) {
+  for (int c = lane * N; c < H; c += kWave * N) {
+    const int at = min(c, H - N);
     float a[N], o[N];
-    load_n<DT, N>(d + (size_t)c * N, a);
+    unpack<DT, N>(*raw<BYTES>(d + at), a);
     if (dw) {
       float y[N];
-      load_n<DT, N, true>(ys + row + (size_t)c * N, y);
+      unpack<DT, N>(__builtin_nontemporal_load(raw<BYTES>(ys + row + at)), y);
+      // (the last chunk's elements that the one before it has counted stay out)
 #pragma unroll
-      for (int i = 0; i < N; ++i) sum = fmaf(a[i], y[i], sum);
+      for (int i = 0; i < N; ++i) sum = at + i >= c ? fmaf(a[i], y[i], sum) : sum;
     }
     if (dys) {
 #pragma unroll
       for (int i = 0; i < N; ++i) o[i] = g * a[i];
-      store_n<DT, N, true>(dys + row + (size_t)c * N, o);
+      __builtin_nontemporal_store(pack<DT, N>(o), raw<BYTES>(dys + row + at));
     }
   }
   if (dw) {
@@ -386,84 +411,76 @@ __global__ __launch_bounds__(kThreads) void k_combine_backward(
 }
 
 template <int BYTES>
-hipError_t dispatch_t(const OrderShape &s, size_t row_bytes, const void *x, const int *ids,
+hipError_t dispatch_t(const OrderShape &s, int row_bytes, const void *x, const int *ids,
                       int *expert_start, int *sorted_rows, int *row_pos, void *xs, int *counts,
                       hipStream_t st) {
-  typedef typename Raw<BYTES>::type V;
-  const int chunks = (int)(row_bytes / BYTES);
-  const V *vx = static_cast<const V *>(x);
-  V *vxs = static_cast<V *>(xs);
+  const char *cx = static_cast<const char *>(x);
+  char *cxs = static_cast<char *>(xs);
   if (s.R <= kFusedRows)
-    return launch_kernel(k_dispatch_fused<BYTES>, dim3(s.R + 1), dim3(kThreads), 0, st, s, chunks, vx,
-                         ids, expert_start, sorted_rows, row_pos, vxs);
+    return launch_kernel(k_dispatch_fused<BYTES>, dim3(s.R + 1), dim3(kThreads), 0, st, s, row_bytes,
+                         cx, ids, expert_start, sorted_rows, row_pos, cxs);
   const int C = order_chunk_rows(s.R), nch = order_chunks(s.R);
   int bits = 0;
   while ((1 << bits) < s.E) ++bits;
   hipError_t e = launch_kernel(k_order_count, dim3(nch), dim3(kThreads), 0, st, s.R, s.E, C, ids, counts);
   if (e != hipSuccess) return e;
   e = launch_kernel(k_order_place, dim3(nch), dim3(kThreads), 0, st, s.R, s.E, C, nch, bits,
-                    bits < 8 ? bits : 8, ids,
-                    static_cast<const int *>(counts), expert_start, sorted_rows, row_pos);
+                    bits < 8 ? bits : 8, ids, static_cast<const int *>(counts), expert_start,
+                    sorted_rows, row_pos);
   if (e != hipSuccess || !xs) return e;
-  const RowGrid g = row_grid(s.T, chunks);
-  return launch_kernel(k_scatter<BYTES>, g.grid, dim3(kThreads), 0, st, s, chunks, g.tpt_shift, vx,
-                       static_cast<const int *>(row_pos), vxs);
+  const RowGrid g = row_grid(s.T, (row_bytes + BYTES - 1) / BYTES);
+  return launch_kernel(k_scatter<BYTES>, g.grid, dim3(kThreads), 0, st, s, row_bytes, g.tpt_shift, cx,
+                       static_cast<const int *>(row_pos), cxs);
 }
 
 template <typename DT, int N>
 hipError_t combine_t(const OrderShape &s, const void *ys, const int *row_pos, const float *w, void *out,
                      hipStream_t st) {
-  const int chunks = s.H / N;
-  const RowGrid g = row_grid(s.T, chunks);
+  const RowGrid g = row_grid(s.T, (s.H + N - 1) / N);
   if (w)
-    return launch_kernel(k_combine_order<DT, N, true>, g.grid, dim3(kThreads), 0, st, s, chunks,
-                         g.tpt_shift, static_cast<const DT *>(ys), row_pos, w, static_cast<DT *>(out));
-  return launch_kernel(k_combine_order<DT, N, false>, g.grid, dim3(kThreads), 0, st, s, chunks,
-                       g.tpt_shift, static_cast<const DT *>(ys), row_pos, w, static_cast<DT *>(out));
+    return launch_kernel(k_combine_order<DT, N, true>, g.grid, dim3(kThreads), 0, st, s, g.tpt_shift,
+                         static_cast<const DT *>(ys), row_pos, w, static_cast<DT *>(out));
+  return launch_kernel(k_combine_order<DT, N, false>, g.grid, dim3(kThreads), 0, st, s, g.tpt_shift,
+                       static_cast<const DT *>(ys), row_pos, w, static_cast<DT *>(out));
 }
 
 template <typename DT, int N>
 hipError_t combine_backward_t(const OrderShape &s, const void *dout, const void *ys, const int *row_pos,
                               const float *w, void *dys, float *dw, hipStream_t st) {
   return launch_kernel(k_combine_backward<DT, N>, dim3((s.R + kWaves - 1) / kWaves), dim3(kThreads), 0,
-                       st, s, s.H / N, static_cast<const DT *>(dout), static_cast<const DT *>(ys),
-                       row_pos, w, static_cast<DT *>(dys), dw);
+                       st, s, static_cast<const DT *>(dout), static_cast<const DT *>(ys), row_pos, w,
+                       static_cast<DT *>(dys), dw);
 }
 
 }  // namespace
 
 int dispatch_counts(int R) { return R <= kFusedRows ? 0 : order_chunks(R); }
 
-// Rows of a multiple of 16 bytes move 16 bytes a lane, others 4 or 2.
+// 16 bytes a lane, or an element where a row is shorter than that.
 hipError_t launch_dispatch(const OrderShape &s, const void *x, const int *ids, int *expert_start,
                            int *sorted_rows, int *row_pos, void *xs, int *counts, hipStream_t st) {
-  const size_t b = (size_t)s.H * (s.bf16 ? 2 : 4);
-  if (b % 16 == 0) return dispatch_t<16>(s, b, x, ids, expert_start, sorted_rows, row_pos, xs, counts, st);
-  if (b % 4 == 0) return dispatch_t<4>(s, b, x, ids, expert_start, sorted_rows, row_pos, xs, counts, st);
+  const int b = s.H * (s.bf16 ? 2 : 4);
+  if (b >= 16) return dispatch_t<16>(s, b, x, ids, expert_start, sorted_rows, row_pos, xs, counts, st);
   return dispatch_t<2>(s, b, x, ids, expert_start, sorted_rows, row_pos, xs, counts, st);
 }
 
 hipError_t launch_combine_rows(const OrderShape &s, const void *ys, const int *row_pos, const float *w,
                                void *out, hipStream_t st) {
-  if (s.bf16) {
-    if (s.H % 8 == 0) return combine_t<uint16_t, 8>(s, ys, row_pos, w, out, st);
-    if (s.H % 2 == 0) return combine_t<uint16_t, 2>(s, ys, row_pos, w, out, st);
-    return combine_t<uint16_t, 1>(s, ys, row_pos, w, out, st);
-  }
-  if (s.H % 4 == 0) return combine_t<float, 4>(s, ys, row_pos, w, out, st);
-  return combine_t<float, 1>(s, ys, row_pos, w, out, st);
+  if (s.bf16)
+    return s.H >= 8 ? combine_t<uint16_t, 8>(s, ys, row_pos, w, out, st)
+                    : combine_t<uint16_t, 1>(s, ys, row_pos, w, out, st);
+  return s.H >= 4 ? combine_t<float, 4>(s, ys, row_pos, w, out, st)
+                  : combine_t<float, 1>(s, ys, row_pos, w, out, st);
 }
 
 hipError_t launch_combine_backward(const OrderShape &s, const void *dout, const void *ys,
                                    const int *row_pos, const float *w, void *dys, float *dw,
                                    hipStream_t st) {
-  if (s.bf16) {
-    if (s.H % 8 == 0) return combine_backward_t<uint16_t, 8>(s, dout, ys, row_pos, w, dys, dw, st);
-    if (s.H % 2 == 0) return combine_backward_t<uint16_t, 2>(s, dout, ys, row_pos, w, dys, dw, st);
-    return combine_backward_t<uint16_t, 1>(s, dout, ys, row_pos, w, dys, dw, st);
-  }
-  if (s.H % 4 == 0) return combine_backward_t<float, 4>(s, dout, ys, row_pos, w, dys, dw, st);
-  return combine_backward_t<float, 1>(s, dout, ys, row_pos, w, dys, dw, st);
+  if (s.bf16)
+    return s.H >= 8 ? combine_backward_t<uint16_t, 8>(s, dout, ys, row_pos, w, dys, dw, st)
+                    : combine_backward_t<uint16_t, 1>(s, dout, ys, row_pos, w, dys, dw, st);
+  return s.H >= 4 ? combine_backward_t<float, 4>(s, dout, ys, row_pos, w, dys, dw, st)
+                  : combine_backward_t<float, 1>(s, dout, ys, row_pos, w, dys, dw, st);
 }
 
 }  // namespace moelora

@@ -97,7 +97,8 @@ def test_no_tokens():
     (1, 1, 1, 1, "uniform"), (1, 2880, 32, 4, "distinct"), (16, 2880, 32, 4, "distinct"),
     (7, 77, 5, 3, "dropped"), (33, 130, 8, 2, "dropped"), (700, 264, 16, 4, "dropped"),
     (2100, 33, 16, 2, "uniform"), (900, 1030, 8, 3, "dropped"), (1500, 8, 300, 2, "uniform"),
-    (400, 2050, 4, 32, "dropped")])
+    (400, 2050, 4, 32, "dropped"), (9, 3, 4, 2, "dropped"), (1200, 5, 4, 2, "uniform"),
+    (50, 9, 4, 2, "dropped"), (5, 517, 4, 3, "dropped")])
 def test_copy_combine_and_gradients(T, H, E, k, kind, dtype):
     rng = np.random.default_rng(T + H)
     ids = make_ids(kind, T, E, k, rng)
@@ -279,7 +280,8 @@ def test_rows_past_32_bit_offsets():
     lib.moelora_combine(T, H, k, lib.BF16, xs, pos, torch.full((T, k), 0.25, device="cuda"), out)
     assert torch.equal(out, x)
     dw = torch.zeros(T, k, device="cuda")
-    lib.moelora_combine_backward(T, H, k, lib.BF16, out, xs, pos, torch.ones_like(dw), xs, dw)
+    lib.moelora_combine_backward(T, H, k, lib.BF16, out, xs, pos, torch.ones_like(dw),
+                                 torch.empty_like(xs), dw)
     assert torch.equal(dw[:, 0].double(), x[:, 0].double() ** 2 * H)
 
 
