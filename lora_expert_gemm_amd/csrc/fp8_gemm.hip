@@ -67,18 +67,20 @@ template <> struct Block<true> {
   }
 };
 
-// Four consecutive outputs of a row, n .. n + 3 of N.
+// Four consecutive outputs of a row, n .. n + 3 of N: one store, which needs
+// no alignment beyond the element's here, or the row's last few by themselves.
 template <typename OT>
 __device__ __forceinline__ void store4(OT *row, int n, int N, const float *v) {
+  typedef uint32_t words __attribute__((ext_vector_type(sizeof(OT))));
+  typedef words mem __attribute__((aligned(2)));
   OT o[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if constexpr (sizeof(OT) == 2) o[i] = __builtin_bit_cast(uint16_t, (__bf16)v[i]);  // nearest even
     else o[i] = v[i];
   }
-  if (N % 4 == 0) {  // (then n + 3 < N, and the four are aligned)
-    if constexpr (sizeof(OT) == 2) *reinterpret_cast<uint2 *>(row + n) = __builtin_bit_cast(uint2, o);
-    else *reinterpret_cast<u32x4_t *>(row + n) = __builtin_bit_cast(u32x4_t, o);
+  if (n + 4 <= N) {
+    *reinterpret_cast<mem *>(row + n) = __builtin_bit_cast(words, o);
   } else {
     for (int i = 0; i < 4; ++i)
       if (n + i < N) row[n + i] = o[i];
