@@ -114,7 +114,7 @@ __device__ __forceinline__ int row_bound(const int *start, int e, int R) {
 // instruction, the address unit and not HBM set the pace.  Tokens, few and
 // shared by all workgroups, come from cache into registers.  Bound by the
 // weights' bytes: the 16-token decode step of 32 experts (392 MB of 23 experts
-// hit) takes 56-59 us, 6.6 TB/s (77 us with the weights straight into
+// hit) takes 56-62 us, 6.6 TB/s (77 us with the weights straight into
 // registers; 75 us with a ring of 4 blocks, whose 64 KB leave two workgroups
 // on a CU where 2 blocks leave four), one row of 4096 -> 11008 (45 MB) 9.8 us.
 constexpr int kSWaves = 4;
@@ -630,7 +630,8 @@ hipError_t gemm_t(const Fp8GemmArgs &a, hipStream_t st) {
   // past the caches then (16-row experts of 128: 78 -> 70 us, g64 94 -> 83,
   // g256 109 -> 105; with seven row tiles an expert, 471 -> 535).  Not for one
   // expert, whose weights may still lie in the last-level cache (d64 18 -> 24).
-  // (float32, 128 experts of 21 rows, 2050 -> 771: 2x2 56 us, 2x4 61)
+  // (float32, 128 experts of 21 rows, 2050 -> 771: 2x2 56 us, 2x4 61, before
+  // the stores of odd rows took four results at once: 53)
   if (tiled_wgs(a, SILU, 2, 4) >= 160 && (sizeof(OT) == 2 || mean > 24)) {
     if (a.E > 1 && mean <= 40) return tiled_t<2, 4, true, SILU, OT>(a, st);
     return tiled_t<2, 4, false, SILU, OT>(a, st);
