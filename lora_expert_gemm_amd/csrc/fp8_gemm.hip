@@ -106,7 +106,7 @@ __device__ __forceinline__ int row_bound(const int *start, int e, int R) {
 // ---------------------------------------------------------------- few rows
 //
 // A workgroup owns 16 NT weight rows (of each half) of one expert and up to
-// 16 TG of its tokens at a time; its four waves take every fourth block of
+// 16 TG of its tokens at a time (every gridDim.z-th group); its four waves take every fourth block of
 // the contraction and add their sums through LDS in wave order, so that a
 // narrow product still fills the chip.  Each wave streams its weights through
 // an LDS ring of its own, S blocks deep, in whole 128-byte lines (8 lanes a
@@ -175,7 +175,7 @@ __global__ __launch_bounds__(kSThreads) void k_fp8_stream(Fp8GemmArgs a) {
   float ws[HV];
   unsigned char *const ring = smem + wave * (S * SLOT);
 
-  for (int m0 = lo; m0 < hi; m0 += 16 * TG) {
+  for (int m0 = lo + blockIdx.z * 16 * TG; m0 < hi; m0 += gridDim.z * 16 * TG) {
     f32x4_t acc[A][TG];
 #pragma unroll
     for (int i = 0; i < A; ++i)
@@ -559,13 +559,13 @@ __global__ __launch_bounds__(kGThreads, sizeof(OT) == 2 && WT * TT <= 8 ? 3 : 2)
 }
 
 template <int NT, int TG, int S, bool ONCE, bool SILU, typename OT>
-hipError_t stream_t(const Fp8GemmArgs &a, hipStream_t st) {
+hipError_t stream_t(const Fp8GemmArgs &a, hipStream_t st, int splits = 1) {
   constexpr int LDS = kSWaves * S * NT * (SILU ? 2 : 1) * 16 * 128;
   auto kern = k_fp8_stream<NT, TG, S, ONCE, SILU, OT>;
   hipError_t err = hipFuncSetAttribute(reinterpret_cast<const void *>(kern),
                                        hipFuncAttributeMaxDynamicSharedMemorySize, LDS);
   if (err != hipSuccess) return err;
-  return launch_kernel(kern, dim3((a.N + 16 * NT - 1) / (16 * NT), a.E < a.R ? a.E : a.R),
+  return launch_kernel(kern, dim3((a.N + 16 * NT - 1) / (16 * NT), a.E < a.R ? a.E : a.R, splits),
                        dim3(kSThreads), LDS, st, a);
 }
 
@@ -616,8 +616,16 @@ hipError_t gemm_t(const Fp8GemmArgs &a, hipStream_t st) {
   // streamed past it: a single row of 4096 -> 11008 9.9 us against 10.6, the
   // 16-token decode 59 us against 66)
   if (a.E > 1 && mean <= 7) return stream_t<NT, 1, 2, true, SILU, OT>(a, st);
-  if (a.E == 1 && mean <= 16) return stream_t<NT, 1, 2, false, SILU, OT>(a, st);
-  if (a.E == 1 && mean <= 32) return stream_t<NT, 2, 2, false, SILU, OT>(a, st);
+  // One expert, so little work that tiles would leave most of the chip idle:
+  // its row groups go to workgroups of their own, with the weights from cache.
+  // us, a tile's and this: 64 x 4096 -> 2048 12.4 / 6.7, 256 x 4096 -> 1024 16.2 /
+  // 8.4, 1000 x 8000 -> 200 27.9 / 14.2, 128 x 2880 -> 2880 13.1 / 12.2, twice
+  // that 13.4 / 16.6.
+  if (a.E == 1) {
+    const int cols = (a.N + 16 * NT - 1) / (16 * NT), g16 = (a.R + 15) / 16, g32 = (a.R + 31) / 32;
+    if (g16 == 1 || (long long)cols * g16 <= 256) return stream_t<NT, 1, 2, false, SILU, OT>(a, st, g16);
+    if (g32 == 1 || (long long)cols * g32 <= 384) return stream_t<NT, 2, 2, false, SILU, OT>(a, st, g32);
+  }
   if constexpr (sizeof(OT) == 2) {
     if (mean >= 56 && tiled_wgs(a, SILU, 4, 8) >= 512) return tiled_t<4, 8, false, SILU, OT>(a, st);
     if (mean >= 96 && tiled_wgs(a, SILU, 2, 8) >= 512) return tiled_t<2, 8, false, SILU, OT>(a, st);

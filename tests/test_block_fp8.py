@@ -322,7 +322,7 @@ def test_dense_sizes_on_both_sides_of_every_choice():
     for out_dtype in (lib.F32, lib.BF16):
         for silu in (False, True):
             for R, N in ((16, 200), (17, 200), (32, 200), (33, 200), (97, 9000), (128, 9000),
-                         (129, 20000), (260, 20000), (1030, 9000)):
+                         (129, 20000), (260, 20000), (1030, 9000), (600, 300), (1030, 64), (40, 1)):
                 x, xs, w, ws, _ = make([R], N, K, 2 if silu else 1, R + N)
                 out = torch.full((R, N), -7.0, dtype=DT[out_dtype], device="cuda")
                 lib.moelora_fp8_gemm(R, N, K, 1, out_dtype, lib.FP8_SILU_MUL if silu else 0, x, xs, None,
