@@ -615,7 +615,18 @@ hipError_t gemm_t(const Fp8GemmArgs &a, hipStream_t st) {
   // One expert's weights may still lie in the last-level cache, several are
   // streamed past it: a single row of 4096 -> 11008 9.9 us against 10.6, the
   // 16-token decode 59 us against 66)
-  if (a.E > 1 && mean <= 7) return stream_t<NT, 1, 2, true, SILU, OT>(a, st);
+  // Short rows leave the waves that share K there without blocks of their own
+  // and each workgroup little but its start and end; a tile has fewer
+  // workgroups, each with more to write.  us, this and a tile's, 64 experts,
+  // 128 rows, -> 2 x 2880 with SILU by K: 128 23.9 / 11.9, 512 35.7 / 25.1, 768
+  // 40.0 / 35.1, 1024 46.3 / 43.6 (float32 768 40.9 / 37.2, 256 rows -> 2880
+  // 26.8 / 28.4).  With few tiles the longer chain of a tile shows: 8 rows of
+  // 512 -> 2880 5.4 / 6.5 (184 tiles), 128 rows -> 768 6.9 / 6.8 (396).
+  if (a.E > 1 && mean <= 7) {
+    if (a.KB <= (sizeof(OT) == 2 ? 6 : 5) && tiled_wgs(a, SILU, 2, 2) >= 100LL * a.KB)
+      return tiled_t<2, 2, true, SILU, OT>(a, st);
+    return stream_t<NT, 1, 2, true, SILU, OT>(a, st);
+  }
   // One expert, so little work that tiles would leave most of the chip idle:
   // its row groups go to workgroups of their own, with the weights from cache.
   // us, a tile's and this: 64 x 4096 -> 2048 12.4 / 6.7, 256 x 4096 -> 1024 16.2 /

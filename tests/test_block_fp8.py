@@ -331,6 +331,25 @@ def test_dense_sizes_on_both_sides_of_every_choice():
                 check(out, ref, err, R)
 
 
+@pytest.mark.parametrize("K", [90, 640, 700, 769])
+@pytest.mark.parametrize("skew", [False, True])
+def test_few_rows_an_expert_on_both_sides_of_every_choice(K, skew):
+    """Many experts with few rows: short rows take tiles where those fill the
+    chip, long ones and small outputs the streamed kernel."""
+    E = 48
+    counts = [90] + [0] * (E - 1) if skew else [(e * 5) % 7 for e in range(E)]
+    R = sum(counts)
+    for out_dtype in (lib.F32, lib.BF16):
+        for silu in (False, True):
+            for N in (70, 1930):
+                x, xs, w, ws, start = make(counts, N, K, 2 if silu else 1, R + N + K)
+                out = torch.full((R, N), -7.0, dtype=DT[out_dtype], device="cuda")
+                lib.moelora_fp8_gemm(R, N, K, E, out_dtype, lib.FP8_SILU_MUL if silu else 0, x, xs, start,
+                                     w, ws, out)
+                ref, err = product64(x, xs, w, ws, counts, N, K, silu, out_dtype)
+                check(out, ref, err, R)
+
+
 def test_nothing_to_gather():
     """A shard without rows: every index points past the source."""
     codes = torch.full((6, 128), 0xAA, dtype=torch.uint8, device="cuda")
