@@ -30,9 +30,9 @@ if not os.path.exists(LIB_PATH):
 # load a second runtime, and whichever initialises second finds no device.
 # So PyTorch, when installed, is imported before the library is loaded.
 try:
-    import torch  # noqa: F401
+    import torch
 except ImportError:
-    pass
+    torch = None
 
 _lib = ctypes.CDLL(LIB_PATH)
 
@@ -230,36 +230,47 @@ def moelora_timing_end(plan):
 
 
 # ---- stand-alone operators.  A tensor argument is checked before its address
-# is passed on: contiguous, on the current device, elements of the expected
-# size and at least as many as the call reads or writes.
+# is passed on: contiguous, on the current device, of the expected type (where
+# bytes are expected, any type of one byte) and with at least as many elements
+# as the call reads or writes.
+
+_FLT, _BF, _INT = (torch.float32, torch.bfloat16, torch.int32) if torch else (None,) * 3
+_BYTE = None
+
 
 def _where(stream):
     """The stream to enqueue on (None: the current one) and the current device.
     (The stream's address by torch's raw getter: building a Stream object costs
     2.7 us of host time, more than a small call's checks.)"""
+    if torch is None:
+        return _stream(stream), -1
     if stream is not None:
-        return _stream(stream), torch.cuda.current_device() if torch.cuda.is_available() else -1
+        dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+        if isinstance(stream, torch.Stream) and stream.device_index != dev:
+            raise ValueError(f"the stream is on device {stream.device_index}, not on the current device")
+        return _stream(stream), dev
     dev = torch.cuda.current_device()
     return torch._C._cuda_getCurrentRawStream(dev), dev
 
 
-def _buf(t, n, size, dev, name, optional=False):
+def _buf(t, n, dtype, dev, name, optional=False):
     if t is None:
         if optional or n == 0:
             return None
         raise ValueError(f"{name} is required")
     if isinstance(t, int):
         return t
-    if t.numel() < n or t.itemsize != size or not t.is_contiguous():
+    if (t.numel() < n or not t.is_contiguous() or
+            (t.itemsize != 1 if dtype is _BYTE else t.dtype is not dtype)):
         raise ValueError(f"{name}: expected a contiguous tensor of at least {n} elements of "
-                         f"{size} bytes, got {tuple(t.shape)} {t.dtype} strides {t.stride()}")
+                         f"{dtype or 'one byte'}, got {tuple(t.shape)} {t.dtype} strides {t.stride()}")
     if t.get_device() != dev or dev < 0:
         raise ValueError(f"{name} is on {t.device}, not on the current device")
     return t.data_ptr()
 
 
-def _es(dtype):
-    return 4 if dtype == F32 else 2
+def _dt(dtype):
+    return _FLT if dtype == F32 else _BF
 
 
 def moelora_dispatch_workspace(n_tokens, n_experts, top_k):
@@ -273,44 +284,44 @@ def moelora_dispatch_workspace(n_tokens, n_experts, top_k):
 def moelora_dispatch(n_tokens, hidden, n_experts, top_k, dtype, x, topk_ids, expert_start,
                      sorted_rows, row_pos, xs, workspace, workspace_bytes, stream=None):
     st, dev = _where(stream)
-    R, es = n_tokens * top_k, _es(dtype)
+    R, dt = n_tokens * top_k, _dt(dtype)
     _check(_lib.moelora_dispatch(
         n_tokens, hidden, n_experts, top_k, dtype,
-        _buf(x, n_tokens * hidden, es, dev, "x", xs is None), _buf(topk_ids, R, 4, dev, "topk_ids"),
-        _buf(expert_start, n_experts + 1, 4, dev, "expert_start"),
-        _buf(sorted_rows, R, 4, dev, "sorted_rows"), _buf(row_pos, R, 4, dev, "row_pos"),
-        _buf(xs, R * hidden, es, dev, "xs", True),
-        _buf(workspace, workspace_bytes, 1, dev, "workspace", True), workspace_bytes,
+        _buf(x, n_tokens * hidden, dt, dev, "x", xs is None), _buf(topk_ids, R, _INT, dev, "topk_ids"),
+        _buf(expert_start, n_experts + 1, _INT, dev, "expert_start"),
+        _buf(sorted_rows, R, _INT, dev, "sorted_rows"), _buf(row_pos, R, _INT, dev, "row_pos"),
+        _buf(xs, R * hidden, dt, dev, "xs", True),
+        _buf(workspace, workspace_bytes, _BYTE, dev, "workspace", True), workspace_bytes,
         st), "moelora_dispatch")
 
 
 def moelora_dispatch_backward(n_tokens, hidden, top_k, dtype, dxs, row_pos, dx, stream=None):
     st, dev = _where(stream)
-    R, es = n_tokens * top_k, _es(dtype)
+    R, dt = n_tokens * top_k, _dt(dtype)
     _check(_lib.moelora_dispatch_backward(
-        n_tokens, hidden, top_k, dtype, _buf(dxs, R * hidden, es, dev, "dxs"),
-        _buf(row_pos, R, 4, dev, "row_pos"), _buf(dx, n_tokens * hidden, es, dev, "dx"), st),
+        n_tokens, hidden, top_k, dtype, _buf(dxs, R * hidden, dt, dev, "dxs"),
+        _buf(row_pos, R, _INT, dev, "row_pos"), _buf(dx, n_tokens * hidden, dt, dev, "dx"), st),
         "moelora_dispatch_backward")
 
 
 def moelora_combine(n_tokens, hidden, top_k, dtype, ys, row_pos, topk_w, out, stream=None):
     st, dev = _where(stream)
-    R, es = n_tokens * top_k, _es(dtype)
+    R, dt = n_tokens * top_k, _dt(dtype)
     _check(_lib.moelora_combine(
-        n_tokens, hidden, top_k, dtype, _buf(ys, R * hidden, es, dev, "ys"),
-        _buf(row_pos, R, 4, dev, "row_pos"), _buf(topk_w, R, 4, dev, "topk_w"),
-        _buf(out, n_tokens * hidden, es, dev, "out"), st), "moelora_combine")
+        n_tokens, hidden, top_k, dtype, _buf(ys, R * hidden, dt, dev, "ys"),
+        _buf(row_pos, R, _INT, dev, "row_pos"), _buf(topk_w, R, _FLT, dev, "topk_w"),
+        _buf(out, n_tokens * hidden, dt, dev, "out"), st), "moelora_combine")
 
 
 def moelora_combine_backward(n_tokens, hidden, top_k, dtype, dout, ys, row_pos, topk_w, dys, dw,
                              stream=None):
     st, dev = _where(stream)
-    R, es = n_tokens * top_k, _es(dtype)
+    R, dt = n_tokens * top_k, _dt(dtype)
     _check(_lib.moelora_combine_backward(
-        n_tokens, hidden, top_k, dtype, _buf(dout, n_tokens * hidden, es, dev, "dout"),
-        _buf(ys, R * hidden, es, dev, "ys", dw is None), _buf(row_pos, R, 4, dev, "row_pos"),
-        _buf(topk_w, R, 4, dev, "topk_w", dys is None), _buf(dys, R * hidden, es, dev, "dys", True),
-        _buf(dw, R, 4, dev, "dw", True), st), "moelora_combine_backward")
+        n_tokens, hidden, top_k, dtype, _buf(dout, n_tokens * hidden, dt, dev, "dout"),
+        _buf(ys, R * hidden, dt, dev, "ys", dw is None), _buf(row_pos, R, _INT, dev, "row_pos"),
+        _buf(topk_w, R, _FLT, dev, "topk_w", dys is None), _buf(dys, R * hidden, dt, dev, "dys", True),
+        _buf(dw, R, _FLT, dev, "dw", True), st), "moelora_combine_backward")
 
 
 def moelora_quantize_rows(n_rows, width, dtype, x, n_src, rows, row_div, codes, scales,
@@ -318,9 +329,10 @@ def moelora_quantize_rows(n_rows, width, dtype, x, n_src, rows, row_div, codes, 
     st, dev = _where(stream)
     kb = (width + 127) // 128
     _check(_lib.moelora_quantize_rows(
-        n_rows, width, dtype, _buf(x, n_src * width, _es(dtype), dev, "x"), n_src,
-        _buf(rows, n_rows, 4, dev, "rows", True), row_div, _buf(codes, n_rows * kb * 128, 1, dev, "codes"),
-        _buf(scales, n_rows * kb, 4, dev, "scales"), st), "moelora_quantize_rows")
+        n_rows, width, dtype, _buf(x, n_src * width, _dt(dtype), dev, "x"), n_src,
+        _buf(rows, n_rows, _INT, dev, "rows", True), row_div,
+        _buf(codes, n_rows * kb * 128, _BYTE, dev, "codes"),
+        _buf(scales, n_rows * kb, _FLT, dev, "scales"), st), "moelora_quantize_rows")
 
 
 def moelora_quantize_weights(n_mats, rows, width, dtype, w, codes, scales, codes_t=None,
@@ -328,11 +340,11 @@ def moelora_quantize_weights(n_mats, rows, width, dtype, w, codes, scales, codes
     st, dev = _where(stream)
     kb, nb = (width + 127) // 128, (rows + 127) // 128
     _check(_lib.moelora_quantize_weights(
-        n_mats, rows, width, dtype, _buf(w, n_mats * rows * width, _es(dtype), dev, "w"),
-        _buf(codes, n_mats * rows * kb * 128, 1, dev, "codes"),
-        _buf(scales, n_mats * nb * kb, 4, dev, "scales"),
-        _buf(codes_t, n_mats * width * nb * 128, 1, dev, "codes_t", True),
-        _buf(scales_t, n_mats * nb * kb, 4, dev, "scales_t", True), st),
+        n_mats, rows, width, dtype, _buf(w, n_mats * rows * width, _dt(dtype), dev, "w"),
+        _buf(codes, n_mats * rows * kb * 128, _BYTE, dev, "codes"),
+        _buf(scales, n_mats * nb * kb, _FLT, dev, "scales"),
+        _buf(codes_t, n_mats * width * nb * 128, _BYTE, dev, "codes_t", True),
+        _buf(scales_t, n_mats * nb * kb, _FLT, dev, "scales_t", True), st),
         "moelora_quantize_weights")
 
 
@@ -343,11 +355,11 @@ def moelora_fp8_gemm(n_rows, n_out, width, n_experts, out_dtype, flags, codes, s
     mats = n_experts * (2 if flags & FP8_SILU_MUL else 1)
     _check(_lib.moelora_fp8_gemm(
         n_rows, n_out, width, n_experts, out_dtype, flags,
-        _buf(codes, n_rows * kb * 128, 1, dev, "codes"), _buf(scales, n_rows * kb, 4, dev, "scales"),
-        _buf(expert_start, n_experts + 1, 4, dev, "expert_start", True),
-        _buf(w_codes, mats * n_out * kb * 128, 1, dev, "w_codes"),
-        _buf(w_scales, mats * nb * kb, 4, dev, "w_scales"),
-        _buf(out, n_rows * n_out, _es(out_dtype), dev, "out"), st), "moelora_fp8_gemm")
+        _buf(codes, n_rows * kb * 128, _BYTE, dev, "codes"), _buf(scales, n_rows * kb, _FLT, dev, "scales"),
+        _buf(expert_start, n_experts + 1, _INT, dev, "expert_start", True),
+        _buf(w_codes, mats * n_out * kb * 128, _BYTE, dev, "w_codes"),
+        _buf(w_scales, mats * nb * kb, _FLT, dev, "w_scales"),
+        _buf(out, n_rows * n_out, _dt(out_dtype), dev, "out"), st), "moelora_fp8_gemm")
 
 
 class Plan:

@@ -180,6 +180,37 @@ def test_tensor_arguments_are_checked():
         lib.moelora_combine(4, 8, 1, lib.F32, None, A, A, A, stream=0)
 
 
+def test_tensors_of_another_type_are_refused():
+    """The same bytes an element are not enough: float16 rows read as bfloat16
+    would be silently wrong."""
+    f32, f16, i32 = torch.zeros(64), torch.zeros(64, dtype=torch.float16), torch.zeros(64, dtype=torch.int32)
+    wrong = "expected a contiguous tensor"
+    for call in (
+            lambda: lib.moelora_combine(4, 8, 1, lib.BF16, f16, A, A, A, stream=0),
+            lambda: lib.moelora_combine(4, 8, 1, lib.F32, i32, A, A, A, stream=0),
+            lambda: lib.moelora_combine(4, 8, 1, lib.F32, A, f32, A, A, stream=0),
+            lambda: lib.moelora_combine(4, 8, 1, lib.F32, A, A, i32, A, stream=0),
+            lambda: lib.moelora_dispatch(4, 8, 4, 2, lib.F32, A, f32, A, A, A, A, A, 64, stream=0),
+            lambda: lib.moelora_dispatch_backward(4, 8, 2, lib.BF16, f16, A, A, stream=0),
+            lambda: lib.moelora_quantize_rows(4, 8, lib.BF16, f16, 4, None, 1, A, A, stream=0),
+            lambda: lib.moelora_quantize_rows(4, 8, lib.BF16, A, 4, None, 1, f32, A, stream=0),
+            lambda: lib.moelora_quantize_weights(1, 4, 8, lib.BF16, f16, A, A, stream=0),
+            lambda: lib.moelora_fp8_gemm(4, 8, 8, 1, lib.BF16, 0, A, A, f32, A, A, A, stream=0),
+            lambda: lib.moelora_fp8_gemm(4, 8, 8, 1, lib.BF16, 0, A, A, None, A, A, f16, stream=0)):
+        with pytest.raises(ValueError, match=wrong):
+            call()
+
+
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    class Stream:
+        device_index, cuda_stream = 1, 0
+    monkeypatch.setattr(torch, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "is_available", lambda: True)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    with pytest.raises(ValueError, match="stream is on device 1"):
+        lib.moelora_combine(4, 8, 1, lib.F32, A, A, A, A, stream=Stream())
+
+
 def test_entry_points_have_bindings():
     for n in lib.exported_symbols():
         assert hasattr(lib, n), n
