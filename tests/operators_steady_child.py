@@ -44,6 +44,16 @@ def main():
                 ws = torch.zeros(2 * 79, 1, device="cuda")
                 y = torch.zeros(R, N, dtype=td, device="cuda")
                 calls.append(lambda a=(R, N, 128, 1, dt, silu, c, s, None, wc, ws, y): L.moelora_fp8_gemm(*a))
+            # eight experts, few to many rows each; short and long rows
+            for R, K, N in ((4, 100, 900), (48, 100, 9000), (48, 1500, 900), (100, 300, 9000),
+                            (300, 300, 9000), (700, 300, 9000), (2000, 300, 9000)):
+                kb, nb = -(-K // 128), -(-N // 128)
+                c, s = torch.zeros(R, kb * 128, dtype=torch.uint8, device="cuda"), torch.zeros(kb, R, device="cuda")
+                wc = torch.zeros(16 * N, kb * 128, dtype=torch.uint8, device="cuda")
+                ws = torch.zeros(16 * nb, kb, device="cuda")
+                y = torch.zeros(R, N, dtype=td, device="cuda")
+                start = (torch.arange(9, device="cuda") * R // 8).int()
+                calls.append(lambda a=(R, N, K, 8, dt, silu, c, s, start, wc, ws, y): L.moelora_fp8_gemm(*a))
     hip = ctypes.CDLL("libamdhip64.so")
     ver = ctypes.c_int()
     calls[0]()
