@@ -627,16 +627,27 @@ hipError_t gemm_t(const Fp8GemmArgs &a, hipStream_t st) {
       return tiled_t<2, 2, true, SILU, OT>(a, st);
     return stream_t<NT, 1, 2, true, SILU, OT>(a, st);
   }
-  // One expert, so little work that tiles would leave most of the chip idle:
-  // its row groups go to workgroups of their own, with the weights from cache.
-  // us, a tile's and this: 64 x 4096 -> 2048 12.4 / 6.7, 256 x 4096 -> 1024 16.2 /
-  // 8.4, 1000 x 8000 -> 200 27.9 / 14.2, 128 x 2880 -> 2880 13.1 / 12.2, twice
-  // that 13.4 / 16.6.
-  if (a.E == 1) {
-    const int cols = (a.N + 16 * NT - 1) / (16 * NT), g16 = (a.R + 15) / 16, g32 = (a.R + 31) / 32;
-    if (g16 == 1 || (long long)cols * g16 <= 256) return stream_t<NT, 1, 2, false, SILU, OT>(a, st, g16);
-    if (g32 == 1 || (long long)cols * g32 <= 384) return stream_t<NT, 2, 2, false, SILU, OT>(a, st, g32);
-  }
+  // So little work that tiles would leave most of the chip idle: an expert's
+  // row groups go to workgroups of their own, with the weights from cache.
+  // One expert, us, a tile's and this: 64 x 4096 -> 2048 12.4 / 6.7, 256 x 4096 ->
+  // 1024 16.2 / 8.4, 1000 x 8000 -> 200 27.9 / 14.2, 128 x 2880 -> 2880 13.1 / 12.2,
+  // twice that 13.4 / 16.6.  Eight experts, 4096 ->, by rows an expert and
+  // columns: 8, 256 23.5 / 6.5; 8, 2048 25.7 / 14.8; 16, 2048 25.7 / 17.8; 24, 4096
+  // 32.3 / 34.8; 32, 256 16.5 / 8.0; 48, 1024 16.9 / 19.4; 32 experts: 8, 256 24.3 /
+  // 13.2; 32, 256 17.2 / 26.9.  Fuller experts than the mean take more groups: a
+  // launch has room for twice the mean and more where that costs little,
+  // and a workgroup goes on to the next group if that is not enough.
+  const int ne = a.E < a.R ? a.E : a.R, cols = (a.N + 16 * NT - 1) / (16 * NT);
+  auto wgs = [&](int rows) { return cols * ((a.R + (long long)ne * (rows - 1)) / rows); };
+  auto groups = [&](int rows) {
+    const int all = (a.R + rows - 1) / rows, twice = (2 * mean + rows - 1) / rows + 1;
+    const long long room = 1024 / ((long long)cols * ne);
+    return a.E == 1 || all < twice ? all : room > all ? all : room > twice ? (int)room : twice;
+  };
+  if ((a.E == 1 && a.R <= 16) || wgs(16) <= (a.E == 1 ? 256 : 192))
+    return stream_t<NT, 1, 2, false, SILU, OT>(a, st, groups(16));
+  if ((a.E == 1 && a.R <= 32) || wgs(32) <= (a.E == 1 ? 384 : mean <= 24 ? 960 : 192))
+    return stream_t<NT, 2, 2, false, SILU, OT>(a, st, groups(32));
   if constexpr (sizeof(OT) == 2) {
     if (mean >= 56 && tiled_wgs(a, SILU, 4, 8) >= 512) return tiled_t<4, 8, false, SILU, OT>(a, st);
     if (mean >= 96 && tiled_wgs(a, SILU, 2, 8) >= 512) return tiled_t<2, 8, false, SILU, OT>(a, st);

@@ -350,6 +350,23 @@ def test_few_rows_an_expert_on_both_sides_of_every_choice(K, skew):
                 check(out, ref, err, R)
 
 
+@pytest.mark.parametrize("counts", [[17, 0, 33, 64, 1, 30], [260, 0, 0, 1, 0], [16, 16, 16, 16], [0, 0, 100],
+                                    [31, 33, 47, 49, 15, 0, 17, 1], [500] + [0] * 24])
+def test_little_work_of_several_experts(counts):
+    """Few column groups: an expert's row groups go to workgroups of their own,
+    and fuller experts than the mean take several passes."""
+    R, E = sum(counts), len(counts)
+    for out_dtype in (lib.F32, lib.BF16):
+        for silu in (False, True):
+            for N, K in ((1, 500), (70, 1300), (900, 300)):
+                x, xs, w, ws, start = make(counts, N, K, 2 if silu else 1, R + N + K)
+                out = torch.full((R, N), -7.0, dtype=DT[out_dtype], device="cuda")
+                lib.moelora_fp8_gemm(R, N, K, E, out_dtype, lib.FP8_SILU_MUL if silu else 0, x, xs, start,
+                                     w, ws, out)
+                ref, err = product64(x, xs, w, ws, counts, N, K, silu, out_dtype)
+                check(out, ref, err, R)
+
+
 def test_nothing_to_gather():
     """A shard without rows: every index points past the source."""
     codes = torch.full((6, 128), 0xAA, dtype=torch.uint8, device="cuda")
