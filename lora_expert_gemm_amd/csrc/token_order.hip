@@ -183,17 +183,24 @@ __global__ __launch_bounds__(kThreads) void k_order_place(
   }
   // totals, and the chunks before this one: 2^e_shift experts at a time, the
   // chunks dealt over the kThreads >> e_shift threads of an expert
+  constexpr int kBatch = 16;  // counts on their way at once
   const int per = 1 << e_shift, el = tid & (per - 1), gi = tid >> e_shift, G = kThreads >> e_shift;
   int kept = 0;
   for (int e0 = 0; e0 < E; e0 += per) {
     const int e = tid < per ? e0 + tid : E;  // the expert this thread scans for
     int total = 0, mine = 0;
     if (e0 + el < E) {
-#pragma unroll 4
-      for (int c = gi; c < nch; c += G) {
-        const int n = counts[(size_t)c * E + e0 + el];
-        total += n;
-        mine += c < me ? n : 0;
+      for (int c0 = gi; c0 < nch; c0 += kBatch * G) {
+        int n[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+          n[u] = counts[(size_t)min(c0 + u * G, nch - 1) * E + e0 + el];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          const int c = c0 + u * G;
+          total += c < nch ? n[u] : 0;
+          mine += c < me ? n[u] : 0;
+        }
       }
     }
     if (G > 1) {
