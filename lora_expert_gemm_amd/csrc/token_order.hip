@@ -17,8 +17,8 @@
 // (non-temporal), which leaves them to the tokens and to the caller: the copy
 // of 6400 x 2880 bf16 tokens for top-4 45.8 -> 35.6 us with its order (184 MB,
 // 5.2 TB/s), their combine's gradients 75.7 -> 67.2 us (332 MB, 4.9 TB/s),
-// combine 41.6 -> 39.5 us (33.7 with eight rows' loads together); nor does a consumer lose by it (dispatch, a
-// library op, combine and back: 254 -> 247 us).
+// combine 41.6 -> 39.5 us (33.7 with eight rows' loads together); nor does a
+// consumer lose by it (dispatch, a library op, combine and back: 254 -> 247 us).
 #include "common.h"
 #include "kernels.h"
 #include "ops.h"
@@ -292,6 +292,24 @@ RowGrid row_grid(int T, int chunks) {
   return g;
 }
 
+// A store past the caches where the wave, whose lanes store bytes [lo, hi) of
+// `row` together, fills every line that this lane's bytes touch; through them
+// for the lines at its ends, which other waves or rows complete (written past
+// the caches a part at a time they cost HBM a pass each: rows of 2888 bf16,
+// 6000 tokens for top-4, 43.9 -> 34.2 us, their combine's gradients 78.6 -> 59.3;
+// of 2050, 12000 tokens, 71 -> 58; rows of whole lines are as they were).
+template <int BYTES>
+__device__ __forceinline__ void store_past(typename Raw<BYTES>::type v, char *row, int o, int lo, int hi) {
+  constexpr uintptr_t kLine = 128;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(row);
+  if (((a + o) & -kLine) >= a + lo && ((a + o + BYTES - 1) | (kLine - 1)) < a + hi) {
+    __builtin_nontemporal_store(v, raw<BYTES>(row + o));
+    asm volatile("");  // (or the compiler makes one plain store of the two)
+  } else {
+    *raw<BYTES>(row + o) = v;
+  }
+}
+
 // xs[pos(t, j)] = x[t] for every j: a token is read once.
 template <int BYTES>
 __global__ __launch_bounds__(kThreads) void k_scatter(OrderShape s, int row_bytes, int tpt_shift,
@@ -305,10 +323,11 @@ __global__ __launch_bounds__(kThreads) void k_scatter(OrderShape s, int row_byte
   const int o = min(c * BYTES, row_bytes - BYTES);
   const typename Raw<BYTES>::type v = *raw<BYTES>(x + (size_t)t * row_bytes + o);
   const int *pos = row_pos + (size_t)t * s.k;
+  const int side = min(tpt, kWave);  // chunks of this row that the wave stores together
+  const int lo = (c & -side) * BYTES, hi = min(lo + side * BYTES, row_bytes);
   for (int j = 0; j < s.k; ++j) {
     const int p = pos[j];
-    if ((unsigned)p < (unsigned)s.R)
-      __builtin_nontemporal_store(v, raw<BYTES>(xs + (size_t)p * row_bytes + o));
+    if ((unsigned)p < (unsigned)s.R) store_past<BYTES>(v, xs + (size_t)p * row_bytes, o, lo, hi);
   }
 }
 
@@ -407,7 +426,9 @@ __global__ __launch_bounds__(kThreads) void k_combine_backward(
     if (dys) {
 #pragma unroll
       for (int i = 0; i < N; ++i) o[i] = g * a[i];
-      __builtin_nontemporal_store(pack<DT, N>(o), raw<BYTES>(dys + row + at));
+      // (the wave's lanes share c - lane N)
+      store_past<BYTES>(pack<DT, N>(o), reinterpret_cast<char *>(dys + row), at * sizeof(DT),
+                        (c - lane * N) * sizeof(DT), min(c - lane * N + kWave * N, H) * sizeof(DT));
     }
   }
   if (dw) {
