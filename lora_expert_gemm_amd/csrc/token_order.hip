@@ -32,10 +32,10 @@ constexpr int kWaves = kThreads / kWave;
 constexpr int kMaxE = 1024;
 // Up to this many routed rows one launch orders and copies: the workgroup of
 // a row finds the row's place by counting (R comparisons), so that a decode
-// step pays one launch.  us for 2880 bf16 columns on 32 experts, one launch
-// against three: 64 rows 2.6 / 7.2, 1024 4.1 / 8.3, 2048 6.6 / 9.3, 4096
-// 16.1 / 10.9.
-constexpr int kFusedRows = 2048;
+// step pays one launch.  us for 2880 and 80 bf16 columns on 32 experts, one
+// launch against three: 64 rows 2.6 / 7.2, 2800 7.4 / 8.7 and 5.4 / 8.5, 4000 9.3 /
+// 8.7 and 6.9 / 8.7, 6000 15.3 / 10.6.
+constexpr int kFusedRows = 2800;
 
 // What a lane moves at once, and how it lies in memory.  16-byte accesses need
 // no more than 2-byte alignment here, so rows of any length are moved 16 bytes
@@ -85,10 +85,16 @@ __global__ __launch_bounds__(kThreads) void k_dispatch_fused(
       return;
     }
     int n = 0;  // rows before p in the order, this wave's share (uniform)
-    for (int q0 = wave * kWave; q0 < R; q0 += kThreads) {
-      const int q = q0 + lane;
-      const int f = q < R ? ids[q] : -1;
-      n += __popcll(__ballot(held(f, E) && (f < e || (f == e && q < p))));
+    constexpr int kBatch = 8;  // ids on their way at once
+    for (int q0 = wave * kWave; q0 < R; q0 += kBatch * kThreads) {
+      int f[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) f[u] = ids[min(q0 + u * kThreads + lane, R - 1)];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int q = q0 + u * kThreads + lane;
+        n += __popcll(__ballot(q < R && held(f[u], E) && (f[u] < e || (f[u] == e && q < p))));
+      }
     }
     if (lane == 0) part[wave] = n;
     __syncthreads();
@@ -392,19 +398,27 @@ __global__ __launch_bounds__(kThreads) void k_combine_order(
   *raw<BYTES>(out + (size_t)t * s.H + o) = pack<DT, N>(acc);
 }
 
-// One wave per routed row: dys[pos] = w dout[t], dw = <dout[t], ys[pos]>.
-template <typename DT, int N>
+// Up to this many routed rows a workgroup takes one, beyond it one per wave:
+// few rows leave a wave's loads one after the other.  us, one wave a row and
+// four, 2880 bf16 and 4436 float32 columns: 40 rows 6.1 / 5.0 and 16.8 / 7.0, 1200
+// 10.6 / 7.0 and 26.8 / 14.5, 4000 14.4 / 15.0 and 37.5 / 36.1, 8000 21.7 / 25.9 and
+// 61.2 / 65.8.
+constexpr int kSplitRows = 2048;
+
+// W waves per routed row: dys[pos] = w dout[t], dw = <dout[t], ys[pos]>.
+template <typename DT, int N, int W>
 __global__ __launch_bounds__(kThreads) void k_combine_backward(
     OrderShape s, const DT *__restrict__ dout, const DT *__restrict__ ys,
     const int *__restrict__ row_pos, const float *__restrict__ w, DT *__restrict__ dys,
     float *__restrict__ dw) {
   constexpr int BYTES = sizeof(DT) * N;
-  const int lane = threadIdx.x & (kWave - 1);
-  const int p = __builtin_amdgcn_readfirstlane(blockIdx.x * kWaves + threadIdx.x / kWave);
+  __shared__ float part[kWaves];
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  const int p = __builtin_amdgcn_readfirstlane((blockIdx.x * kWaves + wave) / W);
   if (p >= s.R) return;
-  const int pos = row_pos[p], H = s.H;
+  const int pos = row_pos[p], H = s.H, share = wave % W;
   if ((unsigned)pos >= (unsigned)s.R) {
-    if (dw && lane == 0) dw[p] = 0.f;
+    if (dw && lane == 0 && share == 0) dw[p] = 0.f;
     return;
   }
   const float g = w ? w[p] : 1.f;
@@ -412,7 +426,7 @@ __global__ __launch_bounds__(kThreads) void k_combine_backward(
   const size_t row = (size_t)pos * H;
   float sum = 0.f;
 #pragma unroll 2
-  for (int c = lane * N; c < H; c += kWave * N) {
+  for (int c = (share * kWave + lane) * N; c < H; c += W * kWave * N) {
     const int at = min(c, H - N);
     float a[N], o[N];
     unpack<DT, N>(*raw<BYTES>(d + at), a);
@@ -434,7 +448,14 @@ __global__ __launch_bounds__(kThreads) void k_combine_backward(
   if (dw) {
 #pragma unroll
     for (int m = kWave / 2; m > 0; m >>= 1) sum += __shfl_xor(sum, m);
-    if (lane == 0) dw[p] = sum;
+    if constexpr (W > 1) {  // (W = kWaves: the row is the workgroup's)
+      if (lane == 0) part[wave] = sum;
+      __syncthreads();
+      sum = part[0];
+#pragma unroll
+      for (int q = 1; q < W; ++q) sum += part[q];
+    }
+    if (lane == 0 && share == 0) dw[p] = sum;
   }
 }
 
@@ -475,9 +496,13 @@ hipError_t combine_t(const OrderShape &s, const void *ys, const int *row_pos, co
 template <typename DT, int N>
 hipError_t combine_backward_t(const OrderShape &s, const void *dout, const void *ys, const int *row_pos,
                               const float *w, void *dys, float *dw, hipStream_t st) {
-  return launch_kernel(k_combine_backward<DT, N>, dim3((s.R + kWaves - 1) / kWaves), dim3(kThreads), 0,
-                       st, s, static_cast<const DT *>(dout), static_cast<const DT *>(ys), row_pos, w,
-                       static_cast<DT *>(dys), dw);
+  auto run = [&](auto kern, int W) {
+    return launch_kernel(kern, dim3(((long long)s.R * W + kWaves - 1) / kWaves), dim3(kThreads), 0, st, s,
+                         static_cast<const DT *>(dout), static_cast<const DT *>(ys), row_pos, w,
+                         static_cast<DT *>(dys), dw);
+  };
+  if (s.R <= kSplitRows) return run(k_combine_backward<DT, N, kWaves>, kWaves);
+  return run(k_combine_backward<DT, N, 1>, 1);
 }
 
 }  // namespace

@@ -65,10 +65,10 @@ def dispatch(ids, E, x=None, dtype=lib.F32, H=None, stream=None, fill=-7):
     return start, rows, pos, xs
 
 
-# T, E, k: one launch up to 2048 rows, chunks of 1024 rows above
+# T, E, k: one launch up to 2800 rows, chunks of 256 rows and more above
 ORDERS = [(1, 1, 1), (1, 1024, 8), (3, 5, 2), (16, 32, 4), (64, 8, 2), (333, 128, 6), (2048, 7, 1),
           (2049, 7, 1), (513, 1000, 4), (6400, 32, 4), (5000, 1024, 8), (1000, 3, 32),
-          (70001, 64, 5)]
+          (70001, 64, 5), (1400, 40, 2), (2801, 1024, 1), (933, 300, 3), (14800, 37, 8)]
 
 
 @pytest.mark.parametrize("kind", ["uniform", "distinct", "dropped", "one", "none"])
@@ -98,7 +98,11 @@ def test_no_tokens():
     (7, 77, 5, 3, "dropped"), (33, 130, 8, 2, "dropped"), (700, 264, 16, 4, "dropped"),
     (2100, 33, 16, 2, "uniform"), (900, 1030, 8, 3, "dropped"), (1500, 8, 300, 2, "uniform"),
     (400, 2050, 4, 32, "dropped"), (9, 3, 4, 2, "dropped"), (1200, 5, 4, 2, "uniform"),
-    (50, 9, 4, 2, "dropped"), (5, 517, 4, 3, "dropped")])
+    (50, 9, 4, 2, "dropped"), (5, 517, 4, 3, "dropped"),
+    # one row a workgroup and one a wave in the gradients, 2048 rows and beyond
+    (512, 2879, 16, 4, "dropped"), (1025, 1259, 16, 2, "dropped"), (2048, 70, 3, 1, "uniform"),
+    # rows that end inside a 128-byte line, copied by one wave, several and a part of one
+    (3000, 700, 16, 4, "dropped"), (2900, 100, 8, 2, "uniform"), (1500, 2887, 8, 2, "dropped")])
 def test_copy_combine_and_gradients(T, H, E, k, kind, dtype):
     rng = np.random.default_rng(T + H)
     ids = make_ids(kind, T, E, k, rng)
