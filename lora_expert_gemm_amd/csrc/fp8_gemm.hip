@@ -634,7 +634,8 @@ hipError_t gemm_t(const Fp8GemmArgs &a, hipStream_t st) {
   // twice that 13.4 / 16.6.  Eight experts, 4096 ->, by rows an expert and
   // columns: 8, 256 23.5 / 6.5; 8, 2048 25.7 / 14.8; 16, 2048 25.7 / 17.8; 24, 4096
   // 32.3 / 34.8; 32, 256 16.5 / 8.0; 48, 1024 16.9 / 19.4; 32 experts: 8, 256 24.3 /
-  // 13.2; 32, 256 17.2 / 26.9; 19 of 95 rows, 6787 -> 115 float32, 29.0 / 25.1.  Fuller experts than the mean take more groups: a
+  // 13.2; 32, 256 17.2 / 26.9; 19 of 95 rows, 6787 -> 115 float32, 29.0 / 25.1.
+  // Fuller experts than the mean take more groups: a
   // launch has room for twice the mean and more where that costs little,
   // and a workgroup goes on to the next group if that is not enough.
   const int ne = a.E < a.R ? a.E : a.R, cols = (a.N + 16 * NT - 1) / (16 * NT);

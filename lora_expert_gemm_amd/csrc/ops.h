@@ -29,9 +29,9 @@ inline int order_chunks(int R) {
   const int c = order_chunk_rows(R);
   return c ? (R + c - 1) / c : 0;
 }
-// Chunks whose counts launch_dispatch writes (none where one launch orders
-// and copies).
-int dispatch_counts(int R);
+// Chunks whose counts launch_dispatch writes (none where the ids are few enough
+// to be counted where they are needed).
+int dispatch_counts(int R, int E);
 
 hipError_t launch_dispatch(const OrderShape &s, const void *x, const int *ids, int *expert_start,
                            int *sorted_rows, int *row_pos, void *xs, int *counts, hipStream_t st);

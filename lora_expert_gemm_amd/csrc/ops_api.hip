@@ -35,7 +35,7 @@ hipError_t resolve_all() {
   };
   for (int bf16 = 0; bf16 < 2; ++bf16) {
     for (int H : {8, 1}) {  // rows of 16 bytes and more, and shorter ones
-      for (int R : {1, 1 << 20}) {
+      for (int R : {1, 4096, 1 << 20}) {
         const OrderShape s{R, H, 1, 1, R, bf16 != 0};
         need(launch_dispatch(s, f, fi, fi, fi, fi, f, fi, nullptr));
         need(launch_combine_rows(s, f, fi, ff, f, nullptr));
@@ -85,7 +85,7 @@ moelora_status order_shape(int32_t T, int32_t H, int32_t E, int32_t k, int32_t d
   return MOELORA_OK;
 }
 
-size_t dispatch_ws(const OrderShape &s) { return dispatch_counts(s.R) * (size_t)s.E * 4; }
+size_t dispatch_ws(const OrderShape &s) { return dispatch_counts(s.R, s.E) * (size_t)s.E * 4; }
 
 }  // namespace
 

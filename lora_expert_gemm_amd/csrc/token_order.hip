@@ -36,6 +36,12 @@ constexpr int kMaxE = 1024;
 // launch against three: 64 rows 2.6 / 7.2, 2800 7.4 / 8.7 and 5.4 / 8.5, 4000 9.3 /
 // 8.7 and 6.9 / 8.7, 6000 15.3 / 10.6.
 constexpr int kFusedRows = 2800;
+// Beyond that, up to this many, every workgroup of the order counts all the ids
+// itself, which saves the launch that counts; its reads grow with R, those of
+// the counts of all chunks with E.  us with 64 columns, two launches against
+// three: 64 experts, 12000 rows 6.3 / 7.2, 24000 8.2 / 7.4; 256 experts, 32000 9.7 /
+// 10.3, 64000 14.8 / 14.5; 1000 experts, 12000 7.7 / 13.1, 128000 29.9 / 40.7.
+bool counts_itself(int R, int E) { return R <= 128 * (E > 128 ? E : 128); }
 
 // What a lane moves at once, and how it lies in memory.  16-byte accesses need
 // no more than 2-byte alignment here, so rows of any length are moved 16 bytes
@@ -146,7 +152,7 @@ __global__ __launch_bounds__(kThreads) void k_dispatch_fused(
   for (int q = part[0] + tid; q < R; q += kThreads) sorted_rows[q] = R;
 }
 
-// Larger batches, first launch: rows per expert of each chunk of C rows.
+// Large batches, first launch: rows per expert of each chunk of C rows.
 __global__ __launch_bounds__(kThreads) void k_order_count(int R, int E, int C,
                                                           const int *__restrict__ ids,
                                                           int *__restrict__ counts) {
@@ -163,18 +169,20 @@ __global__ __launch_bounds__(kThreads) void k_order_count(int R, int E, int C,
   for (int e = tid; e < E; e += kThreads) counts[(size_t)blockIdx.x * E + e] = hist[e];
 }
 
-// Second launch: places of a chunk's rows.  An expert's first place in the
+// Next launch: places of a chunk's rows, from the counts of all chunks or, with
+// DIRECT, from the ids alone.  An expert's first place in the
 // chunk is the experts before it plus the chunks before this one; the waves
 // take a quarter of the chunk each, in order, 64 rows at a time: lanes with
 // the same expert find each other by ballots over the bits of the id, and a
 // lane's rank is the number of equal lanes below it.
+template <bool DIRECT>
 __global__ __launch_bounds__(kThreads) void k_order_place(
     int R, int E, int C, int nch, int id_bits, int e_shift, const int *__restrict__ ids,
     const int *__restrict__ counts, int *__restrict__ expert_start, int *__restrict__ sorted_rows,
     int *__restrict__ row_pos) {
   __shared__ int next[kWaves][kMaxE];
   __shared__ int before[kMaxE];
-  __shared__ int part[2][kThreads];
+  __shared__ int part[2][DIRECT ? kMaxE : kThreads];
   __shared__ int wsum[kWaves];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
   const int me = blockIdx.x;
@@ -182,20 +190,40 @@ __global__ __launch_bounds__(kThreads) void k_order_place(
   const int quarter = (hi - lo + kWaves - 1) / kWaves;
   const int wlo = min(hi, lo + wave * quarter), whi = min(hi, wlo + quarter);
   for (int e = tid; e < kWaves * kMaxE; e += kThreads) (&next[0][0])[e] = 0;
+  if constexpr (DIRECT)
+    for (int e = tid; e < 2 * kMaxE; e += kThreads) (&part[0][0])[e] = 0;
   __syncthreads();
+  constexpr int kBatch = 16;  // ids or counts on their way at once
+  if constexpr (DIRECT) {  // part[0]: rows before the chunk, part[1]: the others
+    for (int q0 = tid; q0 < R; q0 += kBatch * kThreads) {
+      int f[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) f[u] = ids[min(q0 + u * kThreads, R - 1)];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int q = q0 + u * kThreads;
+        if (q < R && held(f[u], E)) atomicAdd(&part[q >= lo][f[u]], 1);
+      }
+    }
+  }
   for (int q = wlo + lane; q < whi; q += kWave) {
     const int f = ids[q];
     if (held(f, E)) atomicAdd(&next[wave][f], 1);
   }
+  if constexpr (DIRECT) __syncthreads();
   // totals, and the chunks before this one: 2^e_shift experts at a time, the
   // chunks dealt over the kThreads >> e_shift threads of an expert
-  constexpr int kBatch = 16;  // counts on their way at once
   const int per = 1 << e_shift, el = tid & (per - 1), gi = tid >> e_shift, G = kThreads >> e_shift;
   int kept = 0;
   for (int e0 = 0; e0 < E; e0 += per) {
     const int e = tid < per ? e0 + tid : E;  // the expert this thread scans for
     int total = 0, mine = 0;
-    if (e0 + el < E) {
+    if constexpr (DIRECT) {
+      if (e < E) {
+        mine = part[0][e];
+        total = mine + part[1][e];
+      }
+    } else if (e0 + el < E) {
       for (int c0 = gi; c0 < nch; c0 += kBatch * G) {
         int n[kBatch];
 #pragma unroll
@@ -209,7 +237,7 @@ __global__ __launch_bounds__(kThreads) void k_order_place(
         }
       }
     }
-    if (G > 1) {
+    if (!DIRECT && G > 1) {
       part[0][tid] = total;
       part[1][tid] = mine;
       __syncthreads();
@@ -471,11 +499,17 @@ hipError_t dispatch_t(const OrderShape &s, int row_bytes, const void *x, const i
   const int C = order_chunk_rows(s.R), nch = order_chunks(s.R);
   int bits = 0;
   while ((1 << bits) < s.E) ++bits;
-  hipError_t e = launch_kernel(k_order_count, dim3(nch), dim3(kThreads), 0, st, s.R, s.E, C, ids, counts);
-  if (e != hipSuccess) return e;
-  e = launch_kernel(k_order_place, dim3(nch), dim3(kThreads), 0, st, s.R, s.E, C, nch, bits,
-                    bits < 8 ? bits : 8, ids, static_cast<const int *>(counts), expert_start,
-                    sorted_rows, row_pos);
+  hipError_t e;
+  if (counts_itself(s.R, s.E)) {
+    e = launch_kernel(k_order_place<true>, dim3(nch), dim3(kThreads), 0, st, s.R, s.E, C, nch, bits, 8, ids,
+                      static_cast<const int *>(nullptr), expert_start, sorted_rows, row_pos);
+  } else {
+    e = launch_kernel(k_order_count, dim3(nch), dim3(kThreads), 0, st, s.R, s.E, C, ids, counts);
+    if (e != hipSuccess) return e;
+    e = launch_kernel(k_order_place<false>, dim3(nch), dim3(kThreads), 0, st, s.R, s.E, C, nch, bits,
+                      bits < 8 ? bits : 8, ids, static_cast<const int *>(counts), expert_start, sorted_rows,
+                      row_pos);
+  }
   if (e != hipSuccess || !xs) return e;
   const RowGrid g = row_grid(s.T, (row_bytes + BYTES - 1) / BYTES);
   return launch_kernel(k_scatter<BYTES>, g.grid, dim3(kThreads), 0, st, s, row_bytes, g.tpt_shift, cx,
@@ -507,7 +541,7 @@ hipError_t combine_backward_t(const OrderShape &s, const void *dout, const void 
 
 }  // namespace
 
-int dispatch_counts(int R) { return R <= kFusedRows ? 0 : order_chunks(R); }
+int dispatch_counts(int R, int E) { return R <= kFusedRows || counts_itself(R, E) ? 0 : order_chunks(R); }
 
 // 16 bytes a lane, or an element where a row is shorter than that.
 hipError_t launch_dispatch(const OrderShape &s, const void *x, const int *ids, int *expert_start,

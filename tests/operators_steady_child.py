@@ -19,7 +19,7 @@ def main():
     calls = []
     for dt, td in ((L.F32, torch.float32), (L.BF16, torch.bfloat16)):
         for H in (136, 6, 5):
-            for T in (8, 1500):
+            for T in (8, 1500, 9000):
                 k, E = 2, 8
                 x, xs = torch.zeros(T, H, dtype=td, device="cuda"), torch.zeros(T * k, H, dtype=td, device="cuda")
                 ids, start = torch.zeros(T, k, **i32), torch.zeros(E + 1, **i32)

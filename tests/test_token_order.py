@@ -65,10 +65,12 @@ def dispatch(ids, E, x=None, dtype=lib.F32, H=None, stream=None, fill=-7):
     return start, rows, pos, xs
 
 
-# T, E, k: one launch up to 2800 rows, chunks of 256 rows and more above
+# T, E, k: one launch up to 2800 rows; chunks of 256 rows and more above, which
+# count all the ids up to 128 max(E, 128) rows
 ORDERS = [(1, 1, 1), (1, 1024, 8), (3, 5, 2), (16, 32, 4), (64, 8, 2), (333, 128, 6), (2048, 7, 1),
           (2049, 7, 1), (513, 1000, 4), (6400, 32, 4), (5000, 1024, 8), (1000, 3, 32),
-          (70001, 64, 5), (1400, 40, 2), (2801, 1024, 1), (933, 300, 3), (14800, 37, 8)]
+          (70001, 64, 5), (1400, 40, 2), (2801, 1024, 1), (933, 300, 3), (14800, 37, 8),
+          (13000, 300, 4), (70001, 1024, 2), (4096, 128, 4), (16385, 128, 1)]
 
 
 @pytest.mark.parametrize("kind", ["uniform", "distinct", "dropped", "one", "none"])
