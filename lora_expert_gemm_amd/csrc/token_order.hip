@@ -91,17 +91,18 @@ __global__ __launch_bounds__(kThreads) void k_dispatch_fused(
       return;
     }
     int n = 0;  // rows before p in the order, this wave's share (uniform)
-    constexpr int kBatch = 8;  // ids on their way at once
-    for (int q0 = wave * kWave; q0 < R; q0 += kBatch * kThreads) {
+    auto precedes = [&](int q, int f) { return q < R && held(f, E) && (f < e || (f == e && q < p)); };
+    constexpr int kBatch = 8;  // ids on their way at once, where there are many
+    int q0 = wave * kWave + lane;
+    for (; R > 2 * kThreads && q0 - lane < R; q0 += kBatch * kThreads) {
       int f[kBatch];
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) f[u] = ids[min(q0 + u * kThreads + lane, R - 1)];
+      for (int u = 0; u < kBatch; ++u) f[u] = ids[min(q0 + u * kThreads, R - 1)];
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int q = q0 + u * kThreads + lane;
-        n += __popcll(__ballot(q < R && held(f[u], E) && (f[u] < e || (f[u] == e && q < p))));
-      }
+      for (int u = 0; u < kBatch; ++u) n += __popcll(__ballot(precedes(q0 + u * kThreads, f[u])));
     }
+    for (; q0 - lane < R; q0 += kThreads)
+      n += __popcll(__ballot(precedes(q0, q0 < R ? ids[q0] : -1)));
     if (lane == 0) part[wave] = n;
     __syncthreads();
     int pos = 0;
