@@ -16,7 +16,7 @@
 // 16 bytes a lane.  What is written or read once goes past the caches
 // (non-temporal), which leaves them to the tokens and to the caller: the copy
 // of 6400 x 2880 bf16 tokens for top-4 45.8 -> 35.6 us with its order (184 MB,
-// 5.2 TB/s), their combine's gradients 75.7 -> 67.2 us (332 MB, 4.9 TB/s),
+// 5.2 TB/s), their combine's gradients 75.7 -> 63.9 us (332 MB, 5.2 TB/s),
 // combine 41.6 -> 39.5 us (33.7 with eight rows' loads together); nor does a
 // consumer lose by it (dispatch, a library op, combine and back: 254 -> 247 us).
 #include "common.h"
