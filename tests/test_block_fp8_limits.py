@@ -1,0 +1,119 @@
+"""The block-scaled product at the ends of its range, against 64 bits.
+
+Scales: any two finite float32 scales of a block, also where their product is
+no normal float32 though the scaled block sum is."""
+import math
+
+import pytest
+import torch
+
+from test_block_fp8 import DT, TABLE, check, lib, make, product64, say, up
+
+pytestmark = pytest.mark.gpu
+
+# rows of each expert, columns: the streamed kernel with one and two row groups
+# a workgroup, short rows an expert in tiles, tiles of 32, 64 and 128 rows
+SCALED = [([4], 40), ([30], 40), ([3, 0, 5], 40), ([2] * 64, 2880), ([40, 0, 33], 200), ([300], 900),
+          ([90, 70, 0, 110], 3000), ([900], 9000), ([700, 500], 9000)]
+
+
+@pytest.mark.parametrize("counts,N", SCALED)
+@pytest.mark.parametrize("out_dtype", [lib.F32, lib.BF16])
+@pytest.mark.parametrize("silu", [False, True])
+def test_scales_whose_product_leaves_the_range(counts, N, out_dtype, silu):
+    """Every row meets, in one of its blocks, a scale whose product with the
+    weights' is subnormal, zero or infinite, next to blocks of ordinary scales
+    that are all zero codes or must not notice.  Tolerance: product64's, which
+    counts two scalings a block, plus 2^-149 for each block's sum that ends
+    below the normal range and each result that does."""
+    halves, K = 2 if silu else 1, 520
+    R, E, KB, NB = sum(counts), len(counts), up(520) // 128, up(N) // 128
+    x, xs, w, ws, start = make(counts, N, K, halves, 31 + N)
+    # block 0: huge times huge on codes of zero in every third row, else both ordinary
+    # block 1: huge times huge, codes of +-2^-9 only: a normal result
+    # block 2: tiny times tiny times codes near 448: a result at the end of the normal range
+    # block 3: tiny times huge, the product in order
+    # block 4 (8 columns): ordinary, and so the only one that counts beside block 2
+    g = torch.Generator(device="cuda").manual_seed(3)
+    small = torch.randint(0, 2, x.shape, generator=g, device="cuda", dtype=torch.uint8) * 128 + 1
+    x[:, 0:128] = 0
+    xs[0], ws[..., 0] = 2.0 ** 100, 2.0 ** 90
+    x[:, 128:256] = torch.where(torch.arange(128, device="cuda") == 5, small[:, :128], 0)
+    w[..., 128:256] = 1
+    xs[1], ws[..., 1] = 2.0 ** 78, 2.0 ** 54     # product 2^132, block sum 2^-18: 2^114
+    xs[2], ws[..., 2] = 2.0 ** -126, 2.0 ** -20  # a block sum of some 2^20: 2^-126
+    xs[3], ws[..., 3] = 2.0 ** -120, 2.0 ** 110
+    rows = torch.arange(R, device="cuda")
+    plain = rows % 3 == 1                        # rows of the first kind: nothing but blocks 0 and 4
+    x[plain, 128:512] = 0
+    tiny = rows % 3 == 2                         # rows of block 2 alone
+    x[tiny, 0:256], x[tiny, 384:] = 0, 0
+    out = torch.full((R, N), -7.0, dtype=DT[out_dtype], device="cuda")
+    say(f"[fp8] scales {counts} N={N} silu={silu} {DT[out_dtype]}")
+    lib.moelora_fp8_gemm(R, N, K, E, out_dtype, lib.FP8_SILU_MUL if silu else 0, x, xs, start, w, ws, out)
+    if silu:   # (values of 2^114 leave the sigmoid's range on either side: the ordinary rows count)
+        keep = plain | tiny
+        ref, err = product64(x, xs, w, ws, counts, N, K, True, out_dtype)
+        out, ref, err = out[keep], ref[keep], err[keep]
+    else:
+        ref, err = product64(x, xs, w, ws, counts, N, K, False, out_dtype)
+    # (bf16 below 2^-126 has steps of 2^-133)
+    err = err + (KB + 1) * 2.0 ** -149 + (2.0 ** -134 if out_dtype == lib.BF16 else 0)
+    check(out, ref, err, out.shape[0])
+
+
+@pytest.mark.parametrize("R,N", [(2, 16), (400, 16), (400, 9000)])
+@pytest.mark.parametrize("out_dtype", [lib.F32, lib.BF16])
+def test_one_product_at_extreme_scales(R, N, out_dtype):
+    """One non-zero product a row, so the result is one number: to a step of
+    float32 and half a step of the result's type."""
+    half = torch.finfo(DT[out_dtype]).eps / 2
+    for sx, sw, cx, cw in ((2.0 ** 100, 2.0 ** 100, 0, 0x38), (2.0 ** 80, 2.0 ** 60, 1, 1),
+                           (2.0 ** -126, 2.0 ** -25, 0x7e, 0x7e), (2.0 ** -126, 1.1e-4, 0x7e, 0x7e),
+                           (1.1e-4, 2.0 ** -126, 0x7e, 0x7e), (2.0 ** 60, 2.0 ** 80, 1, 1),
+                           (-2.0 ** 100, 2.0 ** 100, 0, 0x38), (0.0, 2.0 ** 120, 0x7e, 0x7e),
+                           (2.0 ** 120, 0.0, 0x7e, 0x7e), (2.0 ** -149, 1e30, 0x7e, 0x7e)):
+        x = torch.zeros(R, 128, dtype=torch.uint8, device="cuda")
+        w = torch.zeros(N, 128, dtype=torch.uint8, device="cuda")
+        x[:, 77], w[:, 77] = cx, cw
+        out = torch.full((R, N), -7.0, dtype=DT[out_dtype], device="cuda")
+        xs = torch.full((1, R), sx, device="cuda")
+        ws = torch.full((up(N) // 128, 1), sw, device="cuda")
+        lib.moelora_fp8_gemm(R, N, 128, 1, out_dtype, 0, x, xs, None, w, ws, out)
+        want = float(TABLE[cx] * TABLE[cw]) * float(xs[0, 0]) * float(ws[0, 0])
+        tol = (half + 2.0 ** -22) * abs(want) + (2.0 ** -134 if out_dtype == lib.BF16 else 2.0 ** -149)
+        d = (out.double() - want).abs().max()
+        assert math.isfinite(float(d)) and float(d) <= tol, (sx, sw, float(out[0, 0]), want)
+
+
+def test_an_odd_scale_changes_no_other_row():
+    """A row's result does not depend on whether a neighbour's scales need
+    the longer way: bit for bit."""
+    for counts, N in SCALED:
+        for out_dtype in (lib.F32, lib.BF16):
+            R, E = sum(counts), len(counts)
+            x, xs, w, ws, start = make(counts, N, 384, 1, 8)
+            first, second = (torch.zeros(R, N, dtype=DT[out_dtype], device="cuda") for _ in range(2))
+            lib.moelora_fp8_gemm(R, N, 384, E, out_dtype, 0, x, xs, start, w, ws, first)
+            xs[1, ::5] = 2.0 ** -126
+            lib.moelora_fp8_gemm(R, N, 384, E, out_dtype, 0, x, xs, start, w, ws, second)
+            same = [r for r in range(R) if r % 5]
+            assert torch.equal(first[same], second[same])
+
+
+@pytest.mark.parametrize("counts,N", SCALED)
+def test_a_nan_scale_hides_no_odd_one(counts, N):
+    """Rows whose scale is NaN next to rows of zero codes whose scales'
+    product overflows: the latter stay what they are."""
+    for out_dtype in (lib.F32, lib.BF16):
+        R, E = sum(counts), len(counts)
+        x, xs, w, ws, start = make(counts, N, 384, 1, 8)
+        x[:, 128:256] = 0
+        xs[1], ws[..., 1] = 2.0 ** 100, 2.0 ** 100
+        first, second = (torch.zeros(R, N, dtype=DT[out_dtype], device="cuda") for _ in range(2))
+        lib.moelora_fp8_gemm(R, N, 384, E, out_dtype, 0, x, xs, start, w, ws, first)
+        assert bool(torch.isfinite(first).all())
+        bad = torch.arange(R, device="cuda") // 64 % 2 == 0
+        xs[1, bad] = float("nan")
+        lib.moelora_fp8_gemm(R, N, 384, E, out_dtype, 0, x, xs, start, w, ws, second)
+        assert bool(second[bad].isnan().all()) and torch.equal(first[~bad], second[~bad])
