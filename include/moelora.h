@@ -327,7 +327,10 @@ MOELORA_API moelora_status moelora_quantize_weights(int32_t n_mats, int32_t rows
  * Entries of expert_start are clamped into [0, M]; they must not fall.
  * With MOELORA_FP8_SILU_MUL the weights of an expert are two matrices, gate
  * then up (w_codes [E][2][N][P], w_scales [E][2][NB][KB]: mats = 2 E), and
- * out = SiLU(gate) * up. */
+ * out = SiLU(gate) * up: for MOELORA_F32 within 2^-18 of the value that the
+ * float32 gate and up give (and steps of the smallest subnormal), with
+ * sigmoids below 2^-251 as zero; for MOELORA_BF16 (before the rounding) within
+ * (|gate| + 4) 2^-23 of it, with sigmoids below 2^-126 as zero. */
 #define MOELORA_FP8_SILU_MUL 1u
 MOELORA_API moelora_status moelora_fp8_gemm(int32_t n_rows, int32_t n_out, int32_t width,
                                int32_t n_experts, int32_t out_dtype, uint32_t flags,

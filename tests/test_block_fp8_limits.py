@@ -117,3 +117,59 @@ def test_a_nan_scale_hides_no_odd_one(counts, N):
         xs[1, bad] = float("nan")
         lib.moelora_fp8_gemm(R, N, 384, E, out_dtype, 0, x, xs, start, w, ws, second)
         assert bool(second[bad].isnan().all()) and torch.equal(first[~bad], second[~bad])
+
+
+@pytest.mark.parametrize("R,N", [(2, 64), (40, 64), (400, 64), (400, 9000)])
+@pytest.mark.parametrize("out_dtype", [lib.F32, lib.BF16])
+def test_silu_over_the_range_of_gates(R, N, out_dtype):
+    """Gates from -104 to 90, each one float32 product, with small and large
+    up values.  float32 results: e^(-|g| / 2) to three steps of 2^-23, which
+    meets the sigmoid's denominator squared and both factors of the numerator, a
+    reciprocal to one step and five roundings: under 27 2^-24 of the value, here
+    2^-19; and a step of the smallest subnormal for each of the three factors
+    that may end there.  bf16 results: the argument of 2^x is one rounded
+    product, |g| 2^-23 of the value, sigmoids below 2^-126 are zero, and the
+    rounding."""
+    half = torch.finfo(DT[out_dtype]).eps / 2
+    x = torch.zeros(R, 128, dtype=torch.uint8, device="cuda")
+    x[:, 0], x[:, 64] = 0x38, 0x38                      # 1.0 and 1.0
+    w = torch.zeros(1, 2, N, 128, dtype=torch.uint8, device="cuda")
+    # gate = s (1 + code), code from 0 to 0.875 in steps of 1/8; up = s' code
+    eighths = torch.tensor([0, 0x20, 0x28, 0x2c, 0x30, 0x32, 0x34, 0x36], dtype=torch.uint8, device="cuda")
+    at = torch.arange(N, device="cuda")
+    w[0, 0, :, 0], w[0, 0, :, 64], w[0, 1, :, 0] = 0x38, eighths[at % 8], 0x38
+    gate_code = 1 + TABLE.cuda()[eighths.long()][at % 8]
+    xs = torch.ones(1, R, device="cuda")
+    for scale in (-0.01, -1.0, -7.3, -17.7, -33.1, -47.0, -55.47, 0.01, 1.0, 20.0, 48.0):
+        for up_scale in (1.0, -3.1e-3, 2.0 ** 100, 3.0 ** 70):
+            ws = torch.tensor([scale, up_scale], device="cuda").view(1, 2, 1, 1).repeat(1, 1, up(N) // 128, 1)
+            out = torch.full((R, N), -7.0, dtype=DT[out_dtype], device="cuda")
+            lib.moelora_fp8_gemm(R, N, 128, 1, out_dtype, lib.FP8_SILU_MUL, x, xs, None, w, ws, out)
+            g = (gate_code * float(ws[0, 0, 0, 0])).float().double()
+            ref = g / (1 + torch.exp(-g)) * float(ws[0, 1, 0, 0])
+            if out_dtype == lib.F32:
+                tol = 2.0 ** -19 * ref.abs() + 3 * 2.0 ** -149
+            else:
+                exact = (g.abs() * 2.0 ** -23 + 2.0 ** -21) * ref.abs() + 2.0 ** -126 * (g * float(ws[0, 1, 0, 0])).abs()
+                tol = half * (ref.abs() + exact) + exact + 2.0 ** -134
+            d = (out.double() - ref).abs()
+            assert bool((d <= tol).all()), (scale, up_scale, float((d / ref.abs()).max()) * 2.0 ** 24)
+
+
+@pytest.mark.parametrize("R", [2, 400])
+@pytest.mark.parametrize("out_dtype", [lib.F32, lib.BF16])
+def test_silu_of_gates_that_are_not_finite(R, out_dtype):
+    """A gate of +infinity gives infinity times up, and huge finite gates what
+    the limit gives; a NaN gate stays NaN."""
+    N = 64
+    x = torch.zeros(R, 128, dtype=torch.uint8, device="cuda")
+    x[:, 3] = 0x38
+    w = torch.zeros(1, 2, N, 128, dtype=torch.uint8, device="cuda")
+    w[:, :, :, 3] = 0x38
+    xs = torch.ones(1, R, device="cuda")
+    for gate, want in ((float("inf"), float("-inf")), (1e30, -2e30), (-1e30, 0.0), (float("nan"), float("nan"))):
+        ws = torch.tensor([gate, -2.0], device="cuda").view(1, 2, 1, 1).contiguous()
+        out = torch.full((R, N), -7.0, dtype=DT[out_dtype], device="cuda")
+        lib.moelora_fp8_gemm(R, N, 128, 1, out_dtype, lib.FP8_SILU_MUL, x, xs, None, w, ws, out)
+        ref = torch.full_like(out, want)
+        assert torch.allclose(out, ref, rtol=torch.finfo(DT[out_dtype]).eps, atol=0, equal_nan=True), (gate, out[0, 0])
