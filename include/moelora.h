@@ -244,8 +244,9 @@ MOELORA_API moelora_status moelora_forward_noalloc(moelora_plan_t plan, int32_t 
  *                       are left as they were.  NULL (x may be NULL
  *                       too): the order only.
  * workspace: moelora_dispatch_workspace bytes (0 for small batches, at
- * most 1024 E), no initialisation; calls that overlap need one each.  n_tokens = 0 writes expert_start
- * (zeros) and reads nothing. */
+ * most 1024 E; enough for every smaller n_tokens of the same n_experts and
+ * top_k too), no initialisation; calls that overlap need one each.
+ * n_tokens = 0 writes expert_start (zeros) and reads nothing. */
 MOELORA_API moelora_status moelora_dispatch_workspace(int32_t n_tokens, int32_t n_experts,
                                int32_t top_k, size_t *workspace_bytes);
 MOELORA_API moelora_status moelora_dispatch(int32_t n_tokens, int32_t hidden, int32_t n_experts,

@@ -19,11 +19,10 @@ struct OrderShape {
 // 1024 rows a chunk took 12.5 instead of 5 us for 25600), but at most
 // kOrderChunks, so that every placing workgroup can add up the counts of the
 // chunks before its own.
-constexpr int kOrderChunks = 256;
+constexpr int kOrderChunks = 256, kOrderMinRows = 256;
 inline int order_chunk_rows(int R) {
-  constexpr int kMin = 256;
   const int c = (R + kOrderChunks - 1) / kOrderChunks;
-  return (c + kMin - 1) / kMin * kMin;
+  return (c + kOrderMinRows - 1) / kOrderMinRows * kOrderMinRows;
 }
 inline int order_chunks(int R) {
   const int c = order_chunk_rows(R);

@@ -86,6 +86,12 @@ moelora_status order_shape(int32_t T, int32_t H, int32_t E, int32_t k, int32_t d
 }
 
 size_t dispatch_ws(const OrderShape &s) { return dispatch_counts(s.R, s.E) * (size_t)s.E * 4; }
+// What a caller is told to keep: enough for every smaller batch as well (past
+// kOrderChunks full chunks the chunks grow and their number falls back).
+size_t dispatch_ws_upto(const OrderShape &s) {
+  const int full = std::min((s.R + kOrderMinRows - 1) / kOrderMinRows, kOrderChunks);
+  return dispatch_counts(s.R, s.E) ? full * (size_t)s.E * 4 : 0;
+}
 
 }  // namespace
 
@@ -96,7 +102,7 @@ moelora_status moelora_dispatch_workspace(int32_t n_tokens, int32_t n_experts, i
   if (!workspace_bytes) return MOELORA_ERR_INVALID_ARG;
   OrderShape s;
   const moelora_status st = order_shape(n_tokens, 1, n_experts, top_k, MOELORA_F32, &s);
-  if (st == MOELORA_OK) *workspace_bytes = dispatch_ws(s);
+  if (st == MOELORA_OK) *workspace_bytes = dispatch_ws_upto(s);
   return st;
 }
 
