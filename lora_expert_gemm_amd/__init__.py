@@ -240,8 +240,8 @@ _BYTE = None
 
 def _where(stream):
     """The stream to enqueue on (None: the current one) and the current device.
-    (The stream's address by torch's raw getter: building a Stream object costs
-    2.7 us of host time, more than a small call's checks.)"""
+    (The stream's address by torch's raw getter where this torch has it: building
+    a Stream object costs 2.7 us of host time, more than a small call's checks.)"""
     if torch is None:
         return _stream(stream), -1
     if stream is not None:
@@ -250,7 +250,8 @@ def _where(stream):
             raise ValueError(f"the stream is on device {stream.device_index}, not on the current device")
         return _stream(stream), dev
     dev = torch.cuda.current_device()
-    return torch._C._cuda_getCurrentRawStream(dev), dev
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(dev) if raw else _stream(None), dev
 
 
 def _buf(t, n, dtype, dev, name, optional=False):
