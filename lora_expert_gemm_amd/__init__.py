@@ -97,8 +97,9 @@ _lib.moelora_combine_backward.argtypes = [_I32] * 4 + [_P] * 7
 _lib.moelora_quantize_rows.argtypes = [_I32] * 3 + [_P, _I32, _P, _I32] + [_P] * 3
 _lib.moelora_quantize_weights.argtypes = [_I32] * 4 + [_P] * 6
 _lib.moelora_fp8_gemm.argtypes = [_I32] * 5 + [_U32] + [_P] * 7
+_lib.moelora_fp8_gemm_info.argtypes = [_I32] * 5 + [_U32, ctypes.c_char_p, ctypes.c_size_t]
 for _n in ("dispatch_workspace", "dispatch", "dispatch_backward", "combine", "combine_backward",
-           "quantize_rows", "quantize_weights", "fp8_gemm"):
+           "quantize_rows", "quantize_weights", "fp8_gemm", "fp8_gemm_info"):
     getattr(_lib, "moelora_" + _n).restype = ctypes.c_int
 
 
@@ -361,6 +362,14 @@ def moelora_fp8_gemm(n_rows, n_out, width, n_experts, out_dtype, flags, codes, s
         _buf(w_codes, mats * n_out * kb * 128, _BYTE, dev, "w_codes"),
         _buf(w_scales, mats * nb * kb, _FLT, dev, "w_scales"),
         _buf(out, n_rows * n_out, _dt(out_dtype), dev, "out"), st), "moelora_fp8_gemm")
+
+
+def moelora_fp8_gemm_info(n_rows, n_out, width, n_experts, out_dtype, flags=0):
+    """-> one line on the kernel that such a product takes."""
+    buf = ctypes.create_string_buffer(128)
+    _check(_lib.moelora_fp8_gemm_info(n_rows, n_out, width, n_experts, out_dtype, flags, buf, len(buf)),
+           "moelora_fp8_gemm_info")
+    return buf.value.decode()
 
 
 class Plan:

@@ -700,10 +700,9 @@ long long tiled_wgs(const Fp8GemmArgs &a, bool silu, int WT, int TT) {
 //   d64      42    29      18    19    23    33
 //   d512    328   217      49    34    35    37
 //   d1024   663   435      90    66    53    58
-template <bool SILU, typename OT>
-hipError_t gemm_t(const Fp8GemmArgs &a, hipStream_t st) {
+Fp8Choice choose(const Fp8GemmArgs &a, bool silu, bool bf16) {
   const int mean = a.R / (a.E < a.R ? a.E : a.R);  // rows an expert, if all are hit
-  constexpr int NT = SILU ? 1 : 2;  // 32 weight rows a workgroup either way
+  const int NT = silu ? 1 : 2;  // 32 weight rows a workgroup either way
   // (several experts: some have twice the mean, and pass their weights twice.
   // One expert's weights may still lie in the last-level cache, several are
   // streamed past it: a single row of 4096 -> 11008 9.9 us against 10.6, the
@@ -716,9 +715,9 @@ hipError_t gemm_t(const Fp8GemmArgs &a, hipStream_t st) {
   // 26.8 / 28.4).  With few tiles the longer chain of a tile shows: 8 rows of
   // 512 -> 2880 5.4 / 6.5 (184 tiles), 128 rows -> 768 6.9 / 6.8 (396).
   if (a.E > 1 && mean <= 7) {
-    if (a.KB <= (sizeof(OT) == 2 ? 6 : 5) && tiled_wgs(a, SILU, 2, 2) >= 100LL * a.KB)
-      return tiled_t<2, 2, true, SILU, OT>(a, st);
-    return stream_t<NT, 1, 2, true, SILU, OT>(a, st);
+    if (a.KB <= (bf16 ? 6 : 5) && tiled_wgs(a, silu, 2, 2) >= 100LL * a.KB)
+      return {Fp8Kernel::kTile2x2Once, 1};
+    return {Fp8Kernel::kStream1Once, 1};
   }
   // So little work that tiles would leave most of the chip idle: an expert's
   // row groups go to workgroups of their own, with the weights from cache.
@@ -739,16 +738,16 @@ hipError_t gemm_t(const Fp8GemmArgs &a, hipStream_t st) {
     return a.E == 1 || all < twice ? all : room > all ? all : room > twice ? (int)room : twice;
   };
   if ((a.E == 1 && a.R <= 16) || wgs(16) <= (a.E == 1 ? 256 : 192))
-    return stream_t<NT, 1, 2, false, SILU, OT>(a, st, groups(16));
+    return {Fp8Kernel::kStream1, groups(16)};
   if ((a.E == 1 && a.R <= 32) || wgs(32) <= (a.E == 1 ? 384 : mean <= 24 ? 960 : a.KB > 24 ? 320 : 192))
-    return stream_t<NT, 2, 2, false, SILU, OT>(a, st, groups(32));
-  if constexpr (sizeof(OT) == 2) {
-    if (mean >= 56 && tiled_wgs(a, SILU, 4, 8) >= 512) return tiled_t<4, 8, false, SILU, OT>(a, st);
-    if (mean >= 96 && tiled_wgs(a, SILU, 2, 8) >= 512) return tiled_t<2, 8, false, SILU, OT>(a, st);
+    return {Fp8Kernel::kStream2, groups(32)};
+  if (bf16) {
+    if (mean >= 56 && tiled_wgs(a, silu, 4, 8) >= 512) return {Fp8Kernel::kTile4x8, 1};
+    if (mean >= 96 && tiled_wgs(a, silu, 2, 8) >= 512) return {Fp8Kernel::kTile2x8, 1};
   } else {
     // float32 results: widened operands leave registers for 64 tokens (the
     // 25600-row gate_up 866 us against 919 with 2x4, g1024 201 against 198)
-    if (mean >= 192 && tiled_wgs(a, SILU, 4, 4) >= 512) return tiled_t<4, 4, false, SILU, OT>(a, st);
+    if (mean >= 192 && tiled_wgs(a, silu, 4, 4) >= 512) return {Fp8Kernel::kTile4x4, 1};
   }
   // Where an expert's rows mostly fit one row tile its weights are read once:
   // past the caches then (16-row experts of 128: 78 -> 70 us, g64 94 -> 83,
@@ -756,46 +755,62 @@ hipError_t gemm_t(const Fp8GemmArgs &a, hipStream_t st) {
   // expert, whose weights may still lie in the last-level cache (d64 18 -> 24).
   // (float32, 128 experts of 21 rows, 2050 -> 771: 2x2 56 us, 2x4 61, before
   // the stores of odd rows took four results at once: 53)
-  if (tiled_wgs(a, SILU, 2, 4) >= 160 && (sizeof(OT) == 2 || mean > 24)) {
-    if (a.E > 1 && mean <= 40) return tiled_t<2, 4, true, SILU, OT>(a, st);
-    return tiled_t<2, 4, false, SILU, OT>(a, st);
+  if (tiled_wgs(a, silu, 2, 4) >= 160 && (bf16 || mean > 24)) {
+    if (a.E > 1 && mean <= 40) return {Fp8Kernel::kTile2x4Once, 1};
+    return {Fp8Kernel::kTile2x4, 1};
   }
-  if (a.E > 1 && mean <= 24) return tiled_t<2, 2, true, SILU, OT>(a, st);
-  return tiled_t<2, 2, false, SILU, OT>(a, st);
+  if (a.E > 1 && mean <= 24) return {Fp8Kernel::kTile2x2Once, 1};
+  return {Fp8Kernel::kTile2x2, 1};
 }
 
-// Every kernel gemm_t can pick (launch sites that only look kernels up).
 template <bool SILU, typename OT>
-hipError_t resolve_t() {
+hipError_t launch_t(const Fp8GemmArgs &a, Fp8Choice c, hipStream_t st) {
   constexpr int NT = SILU ? 1 : 2;
-  Fp8GemmArgs a{};
-  a.R = a.N = a.K = a.E = a.KB = a.NB = 1, a.P = 128;
-  hipError_t e[9] = {stream_t<NT, 1, 2, true, SILU, OT>(a, nullptr),  stream_t<NT, 1, 2, false, SILU, OT>(a, nullptr),
-                     stream_t<NT, 2, 2, false, SILU, OT>(a, nullptr),
-                     tiled_t<2, 2, false, SILU, OT>(a, nullptr),     tiled_t<2, 2, true, SILU, OT>(a, nullptr),
-                     tiled_t<2, 4, false, SILU, OT>(a, nullptr),     tiled_t<2, 4, true, SILU, OT>(a, nullptr)};
-  if constexpr (sizeof(OT) == 2) {
-    e[7] = tiled_t<2, 8, false, SILU, OT>(a, nullptr);
-    e[8] = tiled_t<4, 8, false, SILU, OT>(a, nullptr);
-  } else {
-    e[7] = tiled_t<4, 4, false, SILU, OT>(a, nullptr);
-    e[8] = hipSuccess;
+  switch (c.kernel) {
+    case Fp8Kernel::kStream1Once: return stream_t<NT, 1, 2, true, SILU, OT>(a, st, c.groups);
+    case Fp8Kernel::kStream1: return stream_t<NT, 1, 2, false, SILU, OT>(a, st, c.groups);
+    case Fp8Kernel::kStream2: return stream_t<NT, 2, 2, false, SILU, OT>(a, st, c.groups);
+    case Fp8Kernel::kTile2x2Once: return tiled_t<2, 2, true, SILU, OT>(a, st);
+    case Fp8Kernel::kTile2x2: return tiled_t<2, 2, false, SILU, OT>(a, st);
+    case Fp8Kernel::kTile2x4Once: return tiled_t<2, 4, true, SILU, OT>(a, st);
+    case Fp8Kernel::kTile2x4: return tiled_t<2, 4, false, SILU, OT>(a, st);
+    case Fp8Kernel::kTile2x8:
+      if constexpr (sizeof(OT) == 2) return tiled_t<2, 8, false, SILU, OT>(a, st);
+      break;
+    case Fp8Kernel::kTile4x8:
+      if constexpr (sizeof(OT) == 2) return tiled_t<4, 8, false, SILU, OT>(a, st);
+      break;
+    case Fp8Kernel::kTile4x4:
+      if constexpr (sizeof(OT) == 4) return tiled_t<4, 4, false, SILU, OT>(a, st);
+      break;
   }
-  for (hipError_t r : e)
-    if (r != hipSuccess) return r;
-  return hipSuccess;
+  return hipErrorInvalidValue;
+}
+
+hipError_t launch(const Fp8GemmArgs &a, bool silu, bool bf16, Fp8Choice c, hipStream_t st) {
+  if (silu) return bf16 ? launch_t<true, uint16_t>(a, c, st) : launch_t<true, float>(a, c, st);
+  return bf16 ? launch_t<false, uint16_t>(a, c, st) : launch_t<false, float>(a, c, st);
 }
 
 }  // namespace
 
+Fp8Choice choose_fp8_gemm(const Fp8GemmArgs &a, bool silu, bool bf16) { return choose(a, silu, bf16); }
+
 hipError_t launch_fp8_gemm(const Fp8GemmArgs &a, bool silu, bool bf16, hipStream_t st) {
-  if (silu) return bf16 ? gemm_t<true, uint16_t>(a, st) : gemm_t<true, float>(a, st);
-  return bf16 ? gemm_t<false, uint16_t>(a, st) : gemm_t<false, float>(a, st);
+  return launch(a, silu, bf16, choose(a, silu, bf16), st);
 }
 
 hipError_t resolve_fp8_gemm(bool silu, bool bf16) {
-  if (silu) return bf16 ? resolve_t<true, uint16_t>() : resolve_t<true, float>();
-  return bf16 ? resolve_t<false, uint16_t>() : resolve_t<false, float>();
+  Fp8GemmArgs a{};
+  a.R = a.N = a.K = a.E = a.KB = a.NB = 1, a.P = 128;
+  for (Fp8Kernel k : {Fp8Kernel::kStream1Once, Fp8Kernel::kStream1, Fp8Kernel::kStream2, Fp8Kernel::kTile2x2Once,
+                      Fp8Kernel::kTile2x2, Fp8Kernel::kTile2x4Once, Fp8Kernel::kTile2x4, Fp8Kernel::kTile2x8,
+                      Fp8Kernel::kTile4x8, Fp8Kernel::kTile4x4}) {
+    if (bf16 ? k == Fp8Kernel::kTile4x4 : k == Fp8Kernel::kTile2x8 || k == Fp8Kernel::kTile4x8) continue;
+    const hipError_t e = launch(a, silu, bf16, {k, 1}, nullptr);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace moelora

@@ -69,6 +69,19 @@ struct Fp8GemmArgs {
   int KB, NB;              // blocks of 128 along K and N
   size_t P;                // row pitch in bytes, KB * 128
 };
+// Which kernel a product takes: streamed, with 1 or 2 groups of 16 rows at a
+// time and `groups` workgroups to share an expert's groups, or tiled, with
+// weight tiles x token tiles of 16 a wave; Once: the weights go past the caches.
+enum class Fp8Kernel {
+  kStream1Once, kStream1, kStream2,
+  kTile2x2Once, kTile2x2, kTile2x4Once, kTile2x4, kTile2x8, kTile4x8,  // (x8: bf16 results)
+  kTile4x4,                                                           // float32 results
+};
+struct Fp8Choice {
+  Fp8Kernel kernel;
+  int groups;
+};
+Fp8Choice choose_fp8_gemm(const Fp8GemmArgs &a, bool silu, bool bf16);
 hipError_t launch_fp8_gemm(const Fp8GemmArgs &a, bool silu, bool bf16, hipStream_t st);
 // With tl_resolve_only set: looks up every kernel launch_fp8_gemm can pick.
 hipError_t resolve_fp8_gemm(bool silu, bool bf16);

@@ -3,6 +3,7 @@
 // synchronises or keeps anything between calls.
 #include <algorithm>
 #include <atomic>
+#include <cstdio>
 #include <mutex>
 
 #include "../../include/moelora.h"
@@ -82,6 +83,24 @@ moelora_status order_shape(int32_t T, int32_t H, int32_t E, int32_t k, int32_t d
       (dtype != MOELORA_F32 && dtype != MOELORA_BF16))
     return MOELORA_ERR_UNSUPPORTED;
   *s = OrderShape{T, H, E, k, T * k, dtype == MOELORA_BF16};
+  return MOELORA_OK;
+}
+
+// Sizes of the product; the pointers are left null.
+moelora_status gemm_shape(int32_t n_rows, int32_t n_out, int32_t width, int32_t n_experts, int32_t out_dtype,
+                          uint32_t flags, Fp8GemmArgs *a) {
+  if (n_rows < 0) return MOELORA_ERR_INVALID_ARG;
+  if (n_rows > kMaxRows || n_out < 1 || n_out > kMaxOut || width < 1 || width > kMaxWidth ||
+      n_experts < 1 || n_experts > kMaxE || (flags & ~MOELORA_FP8_SILU_MUL) ||
+      (out_dtype != MOELORA_F32 && out_dtype != MOELORA_BF16))
+    return MOELORA_ERR_UNSUPPORTED;
+  a->R = n_rows;
+  a->N = n_out;
+  a->K = width;
+  a->E = n_experts;
+  a->KB = (width + 127) / 128;
+  a->NB = (n_out + 127) / 128;
+  a->P = row_pitch8(width);
   return MOELORA_OK;
 }
 
@@ -203,33 +222,49 @@ moelora_status moelora_fp8_gemm(int32_t n_rows, int32_t n_out, int32_t width, in
                                 int32_t out_dtype, uint32_t flags, const void *codes, const float *scales,
                                 const int32_t *expert_start, const void *w_codes, const float *w_scales,
                                 void *out, moelora_stream_t stream) {
-  if (n_rows < 0) return MOELORA_ERR_INVALID_ARG;
-  const bool silu = flags & MOELORA_FP8_SILU_MUL;
-  if (n_rows > kMaxRows || n_out < 1 || n_out > kMaxOut || width < 1 || width > kMaxWidth ||
-      n_experts < 1 || n_experts > kMaxE || (flags & ~MOELORA_FP8_SILU_MUL) ||
-      (out_dtype != MOELORA_F32 && out_dtype != MOELORA_BF16))
-    return MOELORA_ERR_UNSUPPORTED;
-  if (n_rows == 0) return MOELORA_OK;
+  Fp8GemmArgs a{};
+  moelora_status st = gemm_shape(n_rows, n_out, width, n_experts, out_dtype, flags, &a);
+  if (st != MOELORA_OK || n_rows == 0) return st;
   if (!ok16(codes) || !ok16(scales) || !opt16(expert_start) || !ok16(w_codes) || !ok16(w_scales) ||
       !ok16(out) || (!expert_start && n_experts != 1))
     return MOELORA_ERR_INVALID_ARG;
-  const moelora_status st = ready();
-  if (st != MOELORA_OK) return st;
-  Fp8GemmArgs a{};
+  if ((st = ready()) != MOELORA_OK) return st;
   a.x = static_cast<const uint8_t *>(codes);
   a.xs = scales;
   a.start = expert_start;
   a.w = static_cast<const uint8_t *>(w_codes);
   a.ws = w_scales;
   a.out = out;
-  a.R = n_rows;
-  a.N = n_out;
-  a.K = width;
-  a.E = n_experts;
-  a.KB = (width + 127) / 128;
-  a.NB = (n_out + 127) / 128;
-  a.P = row_pitch8(width);
-  return from_hip(launch_fp8_gemm(a, silu, out_dtype == MOELORA_BF16, reinterpret_cast<hipStream_t>(stream)));
+  return from_hip(launch_fp8_gemm(a, flags & MOELORA_FP8_SILU_MUL, out_dtype == MOELORA_BF16,
+                                  reinterpret_cast<hipStream_t>(stream)));
+}
+
+moelora_status moelora_fp8_gemm_info(int32_t n_rows, int32_t n_out, int32_t width, int32_t n_experts,
+                                     int32_t out_dtype, uint32_t flags, char *buf, size_t buf_len) {
+  Fp8GemmArgs a{};
+  const moelora_status st = gemm_shape(n_rows, n_out, width, n_experts, out_dtype, flags, &a);
+  if (st != MOELORA_OK) return st;
+  if (!buf || buf_len == 0) return MOELORA_ERR_INVALID_ARG;
+  if (n_rows == 0) {
+    snprintf(buf, buf_len, "kernel=none");
+    return MOELORA_OK;
+  }
+  const Fp8Choice c = choose_fp8_gemm(a, flags & MOELORA_FP8_SILU_MUL, out_dtype == MOELORA_BF16);
+  const char *name = "";
+  switch (c.kernel) {
+    case Fp8Kernel::kStream1Once: name = "stream1_once"; break;
+    case Fp8Kernel::kStream1: name = "stream1"; break;
+    case Fp8Kernel::kStream2: name = "stream2"; break;
+    case Fp8Kernel::kTile2x2Once: name = "tile2x2_once"; break;
+    case Fp8Kernel::kTile2x2: name = "tile2x2"; break;
+    case Fp8Kernel::kTile2x4Once: name = "tile2x4_once"; break;
+    case Fp8Kernel::kTile2x4: name = "tile2x4"; break;
+    case Fp8Kernel::kTile2x8: name = "tile2x8"; break;
+    case Fp8Kernel::kTile4x8: name = "tile4x8"; break;
+    case Fp8Kernel::kTile4x4: name = "tile4x4"; break;
+  }
+  snprintf(buf, buf_len, "kernel=%s groups=%d", name, c.groups);
+  return MOELORA_OK;
 }
 
 }  // extern "C"
