@@ -121,12 +121,12 @@ __device__ __forceinline__ uint2 codes8(const Raw8<DT> &r, float inv, bool odd) 
   return make_uint2(u[0], u[1]);
 }
 
-// 16 rows a workgroup, up to kUnroll blocks of each: 16 lanes a (row, block).
+// 16 rows a workgroup, up to kBlocks blocks of each: 16 lanes a (row, block).
 // The blocks' loads are all issued before the first is used; the rows'
 // scales of one block are neighbours in memory.
-constexpr int kUnroll = 4;
+constexpr int kBlocks = 4;
 template <typename DT>
-__global__ __launch_bounds__(kThreads) void k_quant_rows(QuantRowsArgs a, int KB, int per_wg) {
+__global__ __launch_bounds__(kThreads) void k_quant_rows(QuantRowsArgs a, int KB) {
   const int g = threadIdx.x / kLanes, l = threadIdx.x % kLanes;
   const int r = blockIdx.x * kGroups + g;
   if (r >= a.M) return;
@@ -138,31 +138,29 @@ __global__ __launch_bounds__(kThreads) void k_quant_rows(QuantRowsArgs a, int KB
   }
   const DT *row = static_cast<const DT *>(a.x) + (size_t)src * a.K;
   uint8_t *out = a.codes + (size_t)r * KB * kBlk;
-  const int b_end = min(KB, ((int)blockIdx.y + 1) * per_wg);
-  for (int b0 = blockIdx.y * per_wg; b0 < b_end; b0 += kUnroll) {
-    Raw8<DT> v[kUnroll];
+  const int b0 = blockIdx.y * kBlocks;
+  Raw8<DT> v[kBlocks];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-      if (b0 + u < b_end) v[u] = load8<DT>(row, (b0 + u) * kBlk + l * 8, a.K);
+  for (int u = 0; u < kBlocks; ++u)
+    if (b0 + u < KB) v[u] = load8<DT>(row, (b0 + u) * kBlk + l * 8, a.K);
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      if (b0 + u >= b_end) break;
-      uint32_t m = amax_bits8(v[u]);
+  for (int u = 0; u < kBlocks; ++u) {
+    if (b0 + u >= KB) break;
+    uint32_t m = amax_bits8(v[u]);
+#pragma unroll
+    for (int d = 1; d < kLanes; d <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
+    const bool odd = m >= kInfBits;  // the same for the block's 16 lanes
+    if (odd) {
+      m = amax_finite8(v[u]);
 #pragma unroll
       for (int d = 1; d < kLanes; d <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
-      const bool odd = m >= kInfBits;  // the same for the block's 16 lanes
-      if (odd) {
-        m = amax_finite8(v[u]);
-#pragma unroll
-        for (int d = 1; d < kLanes; d <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
-      }
-      const int e = scale_exp(m);
-      const uint2 c = codes8(v[u], pow2(-e), odd);
-      __builtin_nontemporal_store(
-          __builtin_bit_cast(unsigned long long, c),
-          reinterpret_cast<unsigned long long *>(out + (size_t)(b0 + u) * kBlk + l * 8));
-      if (l == 0) a.scales[(size_t)(b0 + u) * a.M + r] = pow2(e);
     }
+    const int e = scale_exp(m);
+    const uint2 c = codes8(v[u], pow2(-e), odd);
+    __builtin_nontemporal_store(
+        __builtin_bit_cast(unsigned long long, c),
+        reinterpret_cast<unsigned long long *>(out + (size_t)(b0 + u) * kBlk + l * 8));
+    if (l == 0) a.scales[(size_t)(b0 + u) * a.M + r] = pow2(e);
   }
 }
 
@@ -255,8 +253,8 @@ template <typename DT>
 hipError_t rows_t(const QuantRowsArgs &a, hipStream_t st) {
   const int KB = (a.K + kBlk - 1) / kBlk;
   const int groups = (a.M + kGroups - 1) / kGroups;
-  return launch_kernel(k_quant_rows<DT>, dim3(groups, (KB + kUnroll - 1) / kUnroll), dim3(kThreads),
-                       0, st, a, KB, kUnroll);
+  return launch_kernel(k_quant_rows<DT>, dim3(groups, (KB + kBlocks - 1) / kBlocks), dim3(kThreads), 0, st,
+                       a, KB);
 }
 
 template <typename DT>

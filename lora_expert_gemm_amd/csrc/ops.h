@@ -9,13 +9,13 @@
 
 namespace moelora {
 
-// Routed rows p = t * k + j, R = T * k of them; H elements of `es` bytes a row.
+// Routed rows p = t * k + j, R = T * k of them; rows of H elements, bf16 or float32.
 struct OrderShape {
   int T, H, E, k, R;
   bool bf16;
 };
 
-// Chunks of the two-launch order: 256 rows (64 a wave, one round of ballots:
+// Chunks of the order of larger batches: 256 rows (64 a wave, one round of ballots:
 // 1024 rows a chunk took 12.5 instead of 5 us for 25600), but at most
 // kOrderChunks, so that every placing workgroup can add up the counts of the
 // chunks before its own.

@@ -454,7 +454,6 @@ __global__ __launch_bounds__(kThreads) void k_combine_backward(
   const DT *d = dout + (size_t)(p / s.k) * H;
   const size_t row = (size_t)pos * H;
   float sum = 0.f;
-#pragma unroll 2
   for (int c = (share * kWave + lane) * N; c < H; c += W * kWave * N) {
     const int at = min(c, H - N);
     float a[N], o[N];
