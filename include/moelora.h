@@ -320,10 +320,10 @@ MOELORA_API moelora_status moelora_quantize_weights(int32_t n_mats, int32_t rows
  *   out[m][n] = sum_b scales[b][m] w_scales[e][n/128][b]
  *               sum_{k in block b} codes[m][k] w_codes[e][n][k]
  * in float32, rounded once to out_dtype (MOELORA_F32, MOELORA_BF16), out
- * [M][N].  For MOELORA_BF16 the FP8 matrix core forms the sums over a block,
- * which are off by at most 7 2^-13 of the block's sum of magnitudes (on
- * normal data 1.5e-5 of the result); for MOELORA_F32 the products are exact
- * and summed in float32.  Rows outside every expert's range are left as they were.
+ * [M][N].  For MOELORA_F32 the products are exact and summed in float32.  For
+ * MOELORA_BF16 the FP8 matrix core forms the sums over a block, except where
+ * rows are few: they are off by at most 7 2^-13 of the block's sum of
+ * magnitudes (on normal data 1.5e-5 of the result).  Rows outside every expert's range are left as they were.
  * expert_start = NULL with n_experts = 1: all rows (a dense product).
  * Entries of expert_start are clamped into [0, M]; they must not fall.
  * With MOELORA_FP8_SILU_MUL the weights of an expert are two matrices, gate

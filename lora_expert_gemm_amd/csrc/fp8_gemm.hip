@@ -19,10 +19,16 @@
 // their group of eight and one of 2^2 does not, while between groups the sum
 // is float32; the 16x16x32 form does the same).  A block sum S = sum |x w| is
 // therefore off by at most 7 2^-13 S, and by 1.5e-5 of its own size on
-// normal data: a hundredth of a bf16 rounding, so bf16 results take it.
-// float32 results do not: there the codes are widened to bf16 (exact) and
-// four v_mfma_f32_16x16x32_bf16 form the block sum, whose products and
-// float32 sum measured within 2^-20 of the largest product.
+// normal data: a hundredth of a bf16 rounding, though it moves one bf16 result
+// in fifty to the neighbouring value.  The exact form widens the codes to bf16
+// (exact) and lets four v_mfma_f32_16x16x32_bf16 form the block sum, whose
+// products and float32 sum measured within 2^-20 of the largest product.  It is
+// taken for float32 results, and for the 16-row streamed kernel whatever the
+// type, where it costs next to nothing (16-token decode 60.1 -> 60.4 us, one row
+// 9.84 -> 10.0).  bf16 results of the others take the FP8 form: the exact one
+// costs the streamed kernel of 32 rows up to 11 %, tiles 5 to 55 % (64 tokens of
+// the 32 experts 81 -> 89 us, 512 dense rows 33 -> 52), the 25600-row gate_up
+// product nearly twice the time.
 //
 // Two kernels.  k_fp8_stream: few rows an expert, bound by the weights'
 // bytes.  k_fp8_tiled: many rows, bound by the matrix cores.
@@ -170,7 +176,7 @@ template <int NT, int TG, int S, bool ONCE, bool SILU, typename OT>
 __global__ __launch_bounds__(kSThreads) void k_fp8_stream(Fp8GemmArgs a) {
   constexpr int HV = SILU ? 2 : 1, A = HV * NT;
   constexpr int SLOT = A * 16 * 128;
-  typedef Block<sizeof(OT) == 4> B;
+  typedef Block<sizeof(OT) == 4 || TG == 1> B;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ f32x4_t red[kSWaves][A * TG][kWave];
   const int lane = threadIdx.x & (kWave - 1);

@@ -230,3 +230,22 @@ def test_quantize_many_rows(M, K, dtype):
     assert np.array_equal(scales.double().cpu().numpy(), want.T)
     wc = codes_of(blocks / want[..., None]).reshape(M, -1)
     assert np.array_equal(TABLE.numpy()[codes.cpu().numpy()], TABLE.numpy()[wc])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,N,K", [("few", 70, 1000), ("few", 2050, 8300), ("little", 70, 2880), ("little", 300, 384),
+                                      ("one", 1100, 4096)])
+def test_few_rows_are_summed_in_float32(rows, N, K):
+    """Where the weights' bytes bound the product, bf16 results come from the
+    exact products too: the float32 results, rounded, bit for bit."""
+    counts = [1] if rows == "one" else ROWS[rows]
+    R, E = sum(counts), len(counts)
+    names = [lib.moelora_fp8_gemm_info(R, N, K, E, t).split()[0] for t in (F, B)]
+    assert names[0] == names[1] and names[0].startswith("kernel=stream1")
+    x, xs, w, ws, start = make(counts, N, K, 1, N + K)
+    outs = []
+    for t in (F, B):
+        out = torch.full((R, N), -7.0, dtype=DT[t], device="cuda")
+        lib.moelora_fp8_gemm(R, N, K, E, t, 0, x, xs, start, w, ws, out)
+        outs.append(out)
+    assert torch.equal(outs[0].to(torch.bfloat16), outs[1])
