@@ -272,8 +272,10 @@ MOELORA_API moelora_status moelora_combine(int32_t n_tokens, int32_t hidden, int
 
 /* Gradients of moelora_combine, given dout [T][H]:
  *   dys [R][H]  dys[row_pos[t][j]] = topk_w[t][j] dout[t]; rows that no
- *               routed row points to are left as they were.  NULL: not wanted
- *               (topk_w may then be NULL).
+ *               routed row points to are left as they were.  Positions in
+ *               [0, R) must differ (those of moelora_dispatch do): of a row
+ *               pointed to twice one of the writes stays, not their sum.
+ *               NULL: not wanted (topk_w may then be NULL).
  *   dw [T][k]   float32, <dout[t], ys[row_pos[t][j]]>, 0 for a dropped row.
  *               NULL: not wanted (ys may then be NULL).  */
 MOELORA_API moelora_status moelora_combine_backward(int32_t n_tokens, int32_t hidden,

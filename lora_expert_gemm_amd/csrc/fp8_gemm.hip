@@ -368,7 +368,8 @@ __global__ __launch_bounds__(kSThreads) void k_fp8_stream(Fp8GemmArgs a) {
 // CU, 574 us (the address unit takes 16 rows at 64 bytes an instruction);
 // weights through the wave's own LDS in whole lines, 523 us where the step
 // before took 671 (another card); block sums scaled four MFMAs after they were
-// formed, 484 us; the shorter epilogue, 452-474 us by card: 1.8-1.9 PFLOP/s.
+// formed, 484 us; the shorter epilogue, 452-474 us by card, and the check for
+// odd scales, 463-490: 1.7-1.8 PFLOP/s.
 // The matrix cores are busy 53 % of the cycles, at 1.8 GHz under the card's
 // power limit.  Without its loads the loop keeps them 68 % busy, and leaving
 // out the waits for the loads changes nothing: the loads' own passage
@@ -709,10 +710,12 @@ long long tiled_wgs(const Fp8GemmArgs &a, bool silu, int WT, int TT) {
 Fp8Choice choose(const Fp8GemmArgs &a, bool silu, bool bf16) {
   const int mean = a.R / (a.E < a.R ? a.E : a.R);  // rows an expert, if all are hit
   const int NT = silu ? 1 : 2;  // 32 weight rows a workgroup either way
-  // (several experts: some have twice the mean, and pass their weights twice.
-  // One expert's weights may still lie in the last-level cache, several are
-  // streamed past it: a single row of 4096 -> 11008 9.9 us against 10.6, the
-  // 16-token decode 59 us against 66)
+  // (several experts: some have twice the mean, and pass their weights twice; an
+  // expert with many times the mean passes them once every 16 rows, one after
+  // the other: 896 rows of one of 128 experts, 2880 -> 2 x 2880, 339 us, spread
+  // evenly 332.  One expert's weights may still lie in the last-level cache,
+  // several are streamed past it: a single row of 4096 -> 11008 9.9 us against
+  // 10.6, the 16-token decode 59 us against 66)
   // Short rows leave the waves that share K there without blocks of their own
   // and each workgroup little but its start and end; a tile has fewer
   // workgroups, each with more to write.  us, this and a tile's, 64 experts,
@@ -732,7 +735,12 @@ Fp8Choice choose(const Fp8GemmArgs &a, bool silu, bool bf16) {
   // twice that 13.4 / 16.6.  Eight experts, 4096 ->, by rows an expert and
   // columns: 8, 256 23.5 / 6.5; 8, 2048 25.7 / 14.8; 16, 2048 25.7 / 17.8; 24, 4096
   // 32.3 / 34.8; 32, 256 16.5 / 8.0; 48, 1024 16.9 / 19.4; 32 experts: 8, 256 24.3 /
-  // 13.2; 32, 256 17.2 / 26.9; 19 of 95 rows, 6787 -> 115 float32, 29.0 / 25.1.
+  // 13.2; 32, 256 17.2 / 26.9.  A tile walks the contraction alone, a slab after
+  // the other, while the streamed kernel's four waves share it, so the longer
+  // it is the more work may go there: of 45 sizes past 24 blocks with up to 320
+  // workgroups (8 to 40 experts of 32 to 150 rows, K 3300 to 8192, either type)
+  // 43 took 0.43 to 0.99 of a tile's time and two 1.05; of eleven sizes of 12
+  // blocks eight took 1.03 to 1.33.
   // Fuller experts than the mean take more groups: a
   // launch has room for twice the mean and more where that costs little,
   // and a workgroup goes on to the next group if that is not enough.
@@ -752,15 +760,18 @@ Fp8Choice choose(const Fp8GemmArgs &a, bool silu, bool bf16) {
     if (mean >= 96 && tiled_wgs(a, silu, 2, 8) >= 512) return {Fp8Kernel::kTile2x8, 1};
   } else {
     // float32 results: widened operands leave registers for 64 tokens (the
-    // 25600-row gate_up 866 us against 919 with 2x4, g1024 201 against 198)
+    // 25600-row gate_up 866 us against 919 with 2x4, g1024 201 against 198; since
+    // then 862-905 by card with the longer SiLU and the check for odd scales)
     if (mean >= 192 && tiled_wgs(a, silu, 4, 4) >= 512) return {Fp8Kernel::kTile4x4, 1};
   }
   // Where an expert's rows mostly fit one row tile its weights are read once:
   // past the caches then (16-row experts of 128: 78 -> 70 us, g64 94 -> 83,
   // g256 109 -> 105; with seven row tiles an expert, 471 -> 535).  Not for one
   // expert, whose weights may still lie in the last-level cache (d64 18 -> 24).
-  // (float32, 128 experts of 21 rows, 2050 -> 771: 2x2 56 us, 2x4 61, before
-  // the stores of odd rows took four results at once: 53)
+  // float32 results widen every row of a tile, padding too, so 64-row tiles
+  // want more than 24 rows an expert: time of 2x4 over 2x2 for 32 to 128 experts,
+  // 2050 -> 771, 2880 -> 2880 and 1024 -> 4096, 9 rows 1.01-1.32, 16 0.95-1.17, 24
+  // 0.88-1.04, 28 0.86-1.02, 40 0.83-0.99 (32 experts -> 771 1.19).
   if (tiled_wgs(a, silu, 2, 4) >= 160 && (bf16 || mean > 24)) {
     if (a.E > 1 && mean <= 40) return {Fp8Kernel::kTile2x4Once, 1};
     return {Fp8Kernel::kTile2x4, 1};
