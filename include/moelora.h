@@ -293,7 +293,8 @@ MOELORA_API moelora_status moelora_combine_backward(int32_t n_tokens, int32_t hi
  * The quantisers choose the smallest power of two 2^e >= max|v| / 448 (e >=
  * -126) of the block's finite elements as its scale and round v / 2^e, which
  * is exact, to the nearest code, ties to even; an element that is not finite
- * gets the NaN code.  The product takes any float32 scales.
+ * gets the NaN code.  The product takes any float32 scales; a block whose two
+ * scales multiply to less than 2^-126 may be off by 2^-125.
  * Limits (else MOELORA_ERR_UNSUPPORTED): 1 <= K <= 65536, rows of x <=
  * 2^24, 1 <= N <= 131072, mats <= 65535, E <= 1024. */
 

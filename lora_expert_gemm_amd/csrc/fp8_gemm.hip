@@ -120,23 +120,24 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
 
 // A block sum's two scales are multiplied with each other first: one multiply
 // for a token and a weight block where scaling the sum twice would take one an
-// accumulator.  Where that product is no normal number though neither scale is
-// zero, the sum takes the larger scale first and the other in the
-// multiply-add: block sums of finite codes lie between 2^-18 and 2^25, so
-// whatever the first step loses lies outside float32 after the second.  Rows
-// of zeros get there in earnest (scale 2^-126, times a weight scale below 1).
-// Looking for such scales costs the 25600-row gate_up product 2.5 % (464 ->
-// 476 us), 512 dense rows 1.5 %, the streamed kernel nothing.
-__device__ __forceinline__ bool odd_scale(float product, float a, float b) {
-  constexpr int kNotNormal = 0x2f4;  // +-0, subnormal, infinite
-  return __builtin_amdgcn_classf(product, kNotNormal) && a != 0.f && b != 0.f;
+// accumulator.  Where that product overflows though neither scale is infinite,
+// the sum (of finite codes: 0, or between 2^-18 and 2^25) takes the larger scale
+// first and the other in the multiply-add, so a block of zeros stays zero and a
+// small sum finite.  A product below 2^-126 is rounded by up to 2^-150, which
+// moves its block by up to 2^-125; scaling those twice as well would make up for
+// it, but rows of zeros (scale 2^-126) are among them, and a few of those took
+// the 25600-row gate_up product from 480 to 640 us.  Looking for overflow costs
+// that product 1.7 % (455 -> 463 us), 512 dense rows 1 %, the streamed kernel
+// nothing.
+__device__ __forceinline__ bool overflows(float product) {
+  return __builtin_amdgcn_classf(product, 0x204);  // -inf, +inf
 }
 __device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
-// s: the product of a and b, or the smaller of them where that is odd, with
+// s: the product of a and b, or the smaller of them where that overflows, with
 // the larger in first (1 for the lanes that need nothing: they stay bit for bit
 // what they are without such a neighbour).
 __device__ __forceinline__ void split_scale(float &s, float &first, float a, float b) {
-  const bool odd = odd_scale(s, a, b), a_first = fabsf(a) > fabsf(b);
+  const bool odd = overflows(s), a_first = fabsf(a) > fabsf(b);
   first = odd ? a_first ? a : b : 1.f;
   s = odd ? a_first ? b : a : s;
 }
@@ -160,7 +161,7 @@ __device__ __forceinline__ int row_bound(const int *start, int e, int R) {
 // instruction, the address unit and not HBM set the pace.  Tokens, few and
 // shared by all workgroups, come from cache into registers.  Bound by the
 // weights' bytes: the 16-token decode step of 32 experts (392 MB of 23 experts
-// hit) takes 56-66 us by card, 6.0-6.9 TB/s (77 us with the weights straight into
+// hit) takes 60.5-64 us by card, 6.1-6.5 TB/s (77 us with the weights straight into
 // registers; 75 us with a ring of 4 blocks, whose 64 KB leave two workgroups
 // on a CU where 2 blocks leave four), one row of 4096 -> 11008 (45 MB) 9.8 us.
 constexpr int kSWaves = 4;
@@ -294,7 +295,7 @@ __global__ __launch_bounds__(kSThreads) void k_fp8_stream(Fp8GemmArgs a) {
 #pragma unroll
             for (int h = 0; h < HV; ++h) {
               s[h] = sx[u][t] * sw[h];
-              odd |= odd_scale(s[h], sx[u][t], sw[h]);
+              odd |= overflows(s[h]);
             }
             if (__builtin_expect(__any(odd), 0)) {
 #pragma unroll
@@ -369,7 +370,7 @@ __global__ __launch_bounds__(kSThreads) void k_fp8_stream(Fp8GemmArgs a) {
 // weights through the wave's own LDS in whole lines, 523 us where the step
 // before took 671 (another card); block sums scaled four MFMAs after they were
 // formed, 484 us; the shorter epilogue, 452-474 us by card, and the check for
-// odd scales, 463-490: 1.7-1.8 PFLOP/s.
+// overflowing scales, 460-485: 1.75-1.85 PFLOP/s.
 // The matrix cores are busy 53 % of the cycles, at 1.8 GHz under the card's
 // power limit.  Without its loads the loop keeps them 68 % busy, and leaving
 // out the waits for the loads changes nothing: the loads' own passage
@@ -528,7 +529,7 @@ __global__ __launch_bounds__(kGThreads, sizeof(OT) == 2 && WT * TT <= 8 ? 3 : 2)
   auto add = [&](int i, int t) {
 #pragma unroll
     for (int v = 0; v < 4; ++v) acc[i][t][v] = fmaf(s[SILU ? i / WH : 0], p[i][v], acc[i][t][v]);
-    // (or the compiler sinks the multiply-adds past the branches on odd scales
+    // (or the compiler sinks the multiply-adds past the branches on large scales
     // to the slab's end, and keeps every group's block sums until there)
     asm volatile("" : "+v"(acc[i][t]));
   };
@@ -569,9 +570,8 @@ __global__ __launch_bounds__(kGThreads, sizeof(OT) == 2 && WT * TT <= 8 ? 3 : 2)
     };
     u32x4_t xlo[2], xhi[2];
     read_x(0, xlo[0], xhi[0]);
-    // whether any scale of the slab needs care, all tokens and halves at once
-    // (by the extremes; a scale of zero counts as well, and the products are
-    // right either way)
+    // whether any two scales of the slab overflow, all tokens and halves at once
+    // (by the largest)
     float sxq[SL];
 #pragma unroll
     for (int q = 0; q < SL; ++q) sxq[q] = *reinterpret_cast<const float *>(st + sxat[q]);
@@ -591,13 +591,11 @@ __global__ __launch_bounds__(kGThreads, sizeof(OT) == 2 && WT * TT <= 8 ? 3 : 2)
         if (t == 0 && i == WT - 1) {
 #pragma unroll
           for (int q = 0; q < SL; ++q) asm volatile("" : "+v"(sxq[q]));  // (here, behind the MFMA)
-          uint32_t mn = magnitude(sxq[0]), mx = mn, wmn = magnitude(sw[0]), wmx = wmn;
-          if constexpr (SL > 1) mn = min(mn, magnitude(sxq[SL - 1])), mx = max(mx, magnitude(sxq[SL - 1]));
-          if constexpr (HV > 1) wmn = min(wmn, magnitude(sw[HV - 1])), wmx = max(wmx, magnitude(sw[HV - 1]));
-          const float least = __uint_as_float(mn) * __uint_as_float(wmn);
+          uint32_t mx = magnitude(sxq[0]), wmx = magnitude(sw[0]);
+          if constexpr (SL > 1) mx = max(mx, magnitude(sxq[SL - 1]));
+          if constexpr (HV > 1) wmx = max(wmx, magnitude(sw[HV - 1]));
           const float most = __uint_as_float(mx) * __uint_as_float(wmx);
-          odd = __builtin_amdgcn_ballot_w64(!(least >= __FLT_MIN__)) |  // (NaN too)
-                __builtin_amdgcn_ballot_w64(!(most <= __FLT_MAX__));
+          odd = __builtin_amdgcn_ballot_w64(!(most <= __FLT_MAX__));  // (NaN too)
           __builtin_amdgcn_sched_barrier(0);
         }
       }
@@ -712,7 +710,7 @@ Fp8Choice choose(const Fp8GemmArgs &a, bool silu, bool bf16) {
   const int NT = silu ? 1 : 2;  // 32 weight rows a workgroup either way
   // (several experts: some have twice the mean, and pass their weights twice; an
   // expert with many times the mean passes them once every 16 rows, one after
-  // the other: 896 rows of one of 128 experts, 2880 -> 2 x 2880, 339 us, spread
+  // the other: 896 rows of one of 128 experts, 2880 -> 2 x 2880, 340-360 us, spread
   // evenly 332.  One expert's weights may still lie in the last-level cache,
   // several are streamed past it: a single row of 4096 -> 11008 9.9 us against
   // 10.6, the 16-token decode 59 us against 66)
@@ -761,7 +759,7 @@ Fp8Choice choose(const Fp8GemmArgs &a, bool silu, bool bf16) {
   } else {
     // float32 results: widened operands leave registers for 64 tokens (the
     // 25600-row gate_up 866 us against 919 with 2x4, g1024 201 against 198; since
-    // then 862-905 by card with the longer SiLU and the check for odd scales)
+    // then 862-905 by card with the longer SiLU and the check for overflowing scales)
     if (mean >= 192 && tiled_wgs(a, silu, 4, 4) >= 512) return {Fp8Kernel::kTile4x4, 1};
   }
   // Where an expert's rows mostly fit one row tile its weights are read once:

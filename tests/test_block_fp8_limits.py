@@ -1,7 +1,10 @@
 """The block-scaled product at the ends of its range, against 64 bits.
 
 Scales: any two finite float32 scales of a block, also where their product is
-no normal float32 though the scaled block sum is."""
+no normal float32 though the scaled block sum is.  One that overflows is exact
+all the same.  One below 2^-126 is a multiple of 2^-149, off by at most 2^-150,
+and meets a block sum of at most 128 448^2 < 2^25: its block is off by less than
+2^-125."""
 import math
 
 import pytest
@@ -24,8 +27,9 @@ def test_scales_whose_product_leaves_the_range(counts, N, out_dtype, silu):
     """Every row meets, in one of its blocks, a scale whose product with the
     weights' is subnormal, zero or infinite, next to blocks of ordinary scales
     that are all zero codes or must not notice.  Tolerance: product64's, which
-    counts two scalings a block, plus 2^-149 for each block's sum that ends
-    below the normal range and each result that does."""
+    counts two scalings a block, plus 2^-125 for the one block whose scales'
+    product is below the normal range, plus 2^-149 for each block's sum that ends
+    there and each result that does."""
     halves, K = 2 if silu else 1, 520
     R, E, KB, NB = sum(counts), len(counts), up(520) // 128, up(N) // 128
     x, xs, w, ws, start = make(counts, N, K, halves, 31 + N)
@@ -58,7 +62,7 @@ def test_scales_whose_product_leaves_the_range(counts, N, out_dtype, silu):
     else:
         ref, err = product64(x, xs, w, ws, counts, N, K, False, out_dtype)
     # (bf16 below 2^-126 has steps of 2^-133)
-    err = err + (KB + 1) * 2.0 ** -149 + (2.0 ** -134 if out_dtype == lib.BF16 else 0)
+    err = err + 2.0 ** -125 + (KB + 1) * 2.0 ** -149 + (2.0 ** -134 if out_dtype == lib.BF16 else 0)
     check(out, ref, err, out.shape[0])
 
 
@@ -66,7 +70,8 @@ def test_scales_whose_product_leaves_the_range(counts, N, out_dtype, silu):
 @pytest.mark.parametrize("out_dtype", [lib.F32, lib.BF16])
 def test_one_product_at_extreme_scales(R, N, out_dtype):
     """One non-zero product a row, so the result is one number: to a step of
-    float32 and half a step of the result's type."""
+    float32 and half a step of the result's type, and 2^-125 where the scales'
+    product is below 2^-126."""
     half = torch.finfo(DT[out_dtype]).eps / 2
     for sx, sw, cx, cw in ((2.0 ** 100, 2.0 ** 100, 0, 0x38), (2.0 ** 80, 2.0 ** 60, 1, 1),
                            (2.0 ** -126, 2.0 ** -25, 0x7e, 0x7e), (2.0 ** -126, 1.1e-4, 0x7e, 0x7e),
@@ -81,7 +86,7 @@ def test_one_product_at_extreme_scales(R, N, out_dtype):
         ws = torch.full((up(N) // 128, 1), sw, device="cuda")
         lib.moelora_fp8_gemm(R, N, 128, 1, out_dtype, 0, x, xs, None, w, ws, out)
         want = float(TABLE[cx] * TABLE[cw]) * float(xs[0, 0]) * float(ws[0, 0])
-        tol = (half + 2.0 ** -22) * abs(want) + (2.0 ** -134 if out_dtype == lib.BF16 else 2.0 ** -149)
+        tol = (half + 2.0 ** -22) * abs(want) + (2.0 ** -125 if abs(sx * sw) < 2.0 ** -126 else 0) + (2.0 ** -134 if out_dtype == lib.BF16 else 2.0 ** -149)
         d = (out.double() - want).abs().max()
         assert math.isfinite(float(d)) and float(d) <= tol, (sx, sw, float(out[0, 0]), want)
 
@@ -173,3 +178,27 @@ def test_silu_of_gates_that_are_not_finite(R, out_dtype):
         lib.moelora_fp8_gemm(R, N, 128, 1, out_dtype, lib.FP8_SILU_MUL, x, xs, None, w, ws, out)
         ref = torch.full_like(out, want)
         assert torch.allclose(out, ref, rtol=torch.finfo(DT[out_dtype]).eps, atol=0, equal_nan=True), (gate, out[0, 0])
+
+
+@pytest.mark.parametrize("counts,N", SCALED)
+def test_rows_of_zeros(counts, N):
+    """Padding rows, as the quantiser stores them (codes of zero, scale 2^-126),
+    give zeros and leave the other rows what they are, bit for bit."""
+    K, R, E = 384, sum(counts), len(counts)
+    g = torch.Generator(device="cuda").manual_seed(N)
+    _, _, w, ws, start = make(counts, N, K, 1, 9)
+    v = torch.randn(R, K, generator=g, device="cuda")
+    pad = torch.arange(R, device="cuda") % 3 == 1
+
+    def run(v, dtype):
+        q, s = torch.zeros(R, K, dtype=torch.uint8, device="cuda"), torch.zeros(3, R, device="cuda")
+        lib.moelora_quantize_rows(R, K, lib.F32, v, R, None, 1, q, s)
+        out = torch.full((R, N), -7.0, dtype=DT[dtype], device="cuda")
+        lib.moelora_fp8_gemm(R, N, K, E, dtype, 0, q, s, start, w, ws, out)
+        return out, s
+
+    for dtype in (lib.F32, lib.BF16):
+        full, _ = run(v, dtype)
+        padded, s = run(torch.where(pad[:, None], 0.0, v), dtype)
+        assert bool((s[:, pad] == 2.0 ** -126).all())
+        assert bool((padded[pad] == 0).all()) and torch.equal(padded[~pad], full[~pad])
