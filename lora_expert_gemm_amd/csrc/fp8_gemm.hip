@@ -161,7 +161,7 @@ __device__ __forceinline__ int row_bound(const int *start, int e, int R) {
 // instruction, the address unit and not HBM set the pace.  Tokens, few and
 // shared by all workgroups, come from cache into registers.  Bound by the
 // weights' bytes: the 16-token decode step of 32 experts (392 MB of 23 experts
-// hit) takes 60.5-64 us by card, 6.1-6.5 TB/s (77 us with the weights straight into
+// hit) takes 58-64 us by card, 6.1-6.8 TB/s (77 us with the weights straight into
 // registers; 75 us with a ring of 4 blocks, whose 64 KB leave two workgroups
 // on a CU where 2 blocks leave four), one row of 4096 -> 11008 (45 MB) 9.8 us.
 constexpr int kSWaves = 4;
