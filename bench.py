@@ -73,7 +73,7 @@ def _code_only(text):
 # csrc files that no kernel of the layer is compiled from: the host ABI file
 # and the stand-alone operators
 NOT_LAYER_KERNELS = ("api.hip", "ops_api.hip", "ops.h", "token_order.hip", "block_fp8.hip",
-                     "fp8_gemm.hip")
+                     "fp8_gemm.hip", "grouped.h", "router.hip", "fp4.h", "fp4.hip", "fp4_gemm.hip")
 
 
 def kernel_source_hash(csrc=None):

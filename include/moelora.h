@@ -348,6 +348,117 @@ MOELORA_API moelora_status moelora_fp8_gemm_info(int32_t n_rows, int32_t n_out, 
                                int32_t n_experts, int32_t out_dtype, uint32_t flags,
                                char *buf, size_t buf_len);
 
+/* The router by itself, its losses and their gradient.  logits [T][E] of
+ * dtype; token_mask [T] one byte a token, 0: the token is padding (NULL: no
+ * token is).  An expert is available to a token that is no padding if its logit
+ * is above -inf and not NaN (so -inf switches an expert off); a token with none
+ * counts like padding.  p[t] is the softmax over the available experts, lse[t]
+ * the logarithm of its sum (probabilities below 2^-126 of the largest count as
+ * zero; of several logits of +inf each has the same share).
+ * Limits (else MOELORA_ERR_UNSUPPORTED): 1 <= E <= 1024, 1 <= k <= min(E, 32),
+ * T k <= 2^24.
+ *
+ * moelora_route: the k largest available logits of each token, largest first,
+ * ties to the lower expert index:
+ *   topk_ids [T][k]  -1 where no expert is left (moelora_dispatch drops those)
+ *   topk_w   [T][k]  float32, the softmax over the picked logits, or, with
+ *                    MOELORA_ROUTE_SOFTMAX_ALL, their p; 0 for an id of -1 */
+#define MOELORA_ROUTE_SOFTMAX_ALL 1u
+MOELORA_API moelora_status moelora_route(int32_t n_tokens, int32_t n_experts, int32_t top_k,
+                               int32_t dtype, uint32_t flags, const void *logits,
+                               const uint8_t *token_mask, int32_t *topk_ids, float *topk_w,
+                               moelora_stream_t stream);
+
+/* Per-expert counts and the router's losses over the n tokens that are no
+ * padding:
+ *   counts   [E+1]  picks of each expert (ids outside [0, E) and those of
+ *                   padding do not count); counts[E] = n
+ *   prob_sum [E]    float32, sum over the tokens of p[t][e]
+ *   loss     [2]    float32, E / (k n^2) sum_e counts[e] prob_sum[e] (1 where
+ *                   the experts are used alike) and sum_t lse[t]^2 / n; zeros
+ *                   where n = 0
+ * All are written whole, also for n_tokens = 0, which reads nothing.
+ * workspace: moelora_balance_loss_workspace bytes (0 for small batches, at
+ * most 4096 (E + 2); enough for every smaller n_tokens of the same n_experts
+ * and top_k too), no initialisation; calls that overlap need one each. */
+MOELORA_API moelora_status moelora_balance_loss_workspace(int32_t n_tokens, int32_t n_experts,
+                               int32_t top_k, size_t *workspace_bytes);
+MOELORA_API moelora_status moelora_balance_loss(int32_t n_tokens, int32_t n_experts, int32_t top_k,
+                               int32_t dtype, const void *logits, const uint8_t *token_mask,
+                               const int32_t *topk_ids, int32_t *counts, float *prob_sum,
+                               float *loss, void *workspace, size_t workspace_bytes,
+                               moelora_stream_t stream);
+
+/* The gradient in the logits of the routing weights, of both losses, or of all
+ * three in one pass: dlogits [T][E] of dtype, written whole (zeros for padding
+ * and where an expert is not available).
+ *   dtopk_w [T][k]  float32, the gradient of topk_w (moelora_combine_backward
+ *                   makes it); needs topk_ids and topk_w as moelora_route gave
+ *                   them with the same flags.  Ids outside [0, E) add nothing.
+ *                   NULL: not wanted (topk_ids and topk_w may then be NULL).
+ *   counts [E+1], dloss [2]  of moelora_balance_loss, and the float32 gradients
+ *                   of its two losses.  Counts are constants of the gradient.
+ *                   Summed over several devices, the counts (and, for the
+ *                   loss itself, prob_sum) give the gradient of the loss over
+ *                   all of their tokens.  NULL (both): not wanted. */
+MOELORA_API moelora_status moelora_route_backward(int32_t n_tokens, int32_t n_experts,
+                               int32_t top_k, int32_t dtype, uint32_t flags, const void *logits,
+                               const uint8_t *token_mask, const int32_t *topk_ids,
+                               const float *topk_w, const float *dtopk_w, const int32_t *counts,
+                               const float *dloss, void *dlogits, moelora_stream_t stream);
+
+/* 4-bit weights.  A weight is an E2M1 code (bit 3 the sign; 0, 0.5, 1, 1.5, 2,
+ * 3, 4, 6) times 2^(s - 127), s a byte that the 32 weights of a group along K
+ * share (255: NaN).  A matrix [N][K] is kept in tiles of 16 rows x 128 columns,
+ * NT = ceil(N / 16), KB = ceil(K / 128), KQ = ceil(KB / 4), zeros past N and K:
+ *   codes   [mats][NT][KB][64][16] bytes; of tile (i, j), entry 16 g + r holds
+ *           row 16 i + r, columns 128 j + 32 g .. + 31, two codes a byte, the
+ *           lower column in the low half
+ *   scales  [mats][NT][KQ][64][4] bytes; entry 16 g + r of (i, q) holds the
+ *           scales of that group in tiles 4 q .. 4 q + 3
+ * Limits (else MOELORA_ERR_UNSUPPORTED): 1 <= N <= 131072, 1 <= K <= 65536,
+ * mats <= 65535, mats NT KQ < 2^26.
+ *
+ * From weights w [mats][N][K] of dtype: the scale of a group is the smallest
+ * power of two 2^e >= max|w| / 6 (e >= -125), and w / 2^e, which is exact, is
+ * rounded to the nearest code, ties to even (from 1.75 2^127 on, where that is
+ * 2^128, to the code below).  A group with an element that is not finite gets
+ * the NaN scale and zero codes. */
+MOELORA_API moelora_status moelora_quantize_weights_fp4(int32_t n_mats, int32_t rows,
+                               int32_t width, int32_t dtype, const void *w, void *codes,
+                               void *scales, moelora_stream_t stream);
+
+/* From a checkpoint's row-major form: row_codes [mats][N][ceil(K / 2)] bytes,
+ * two codes each, the lower column in the low half, and row_scales
+ * [mats][N][ceil(K / 32)] bytes. */
+MOELORA_API moelora_status moelora_pack_weights_fp4(int32_t n_mats, int32_t rows, int32_t width,
+                               const void *row_codes, const void *row_scales, void *codes,
+                               void *scales, moelora_stream_t stream);
+
+/* The values w [mats][N][K] that codes and scales stand for.  Both dtypes hold
+ * them exactly (from 2^128 on they are infinite). */
+MOELORA_API moelora_status moelora_dequantize_weights_fp4(int32_t n_mats, int32_t rows,
+                               int32_t width, int32_t dtype, const void *codes,
+                               const void *scales, void *w, moelora_stream_t stream);
+
+/* The grouped product on 4-bit weights: for the rows m of expert e,
+ * expert_start[e] <= m < expert_start[e+1],
+ *   out[m][n] = sum_k x[m][k] w[e][n][k]
+ * with x [M][K] and out [M][N] of dtype; products are exact, summed in float32
+ * and rounded once.  (float32 rows meet the weights in three parts of eight
+ * significant bits: a row with an infinity gives NaN where the sum would be
+ * infinite.)  Rows outside every expert's range are left as they were.
+ * expert_start = NULL with n_experts = 1: all rows (a dense product).
+ * Entries of expert_start are clamped into [0, M]; they must not fall.
+ * With MOELORA_FP4_SILU_MUL the weights of an expert are two matrices, gate
+ * then up (mats = 2 E), and out = SiLU(gate) * up, in float32 as of
+ * moelora_fp8_gemm.  Limits: those of the weights and M <= 2^24, E <= 1024. */
+#define MOELORA_FP4_SILU_MUL 1u
+MOELORA_API moelora_status moelora_fp4_gemm(int32_t n_rows, int32_t n_out, int32_t width,
+                               int32_t n_experts, int32_t dtype, uint32_t flags, const void *x,
+                               const int32_t *expert_start, const void *w_codes,
+                               const void *w_scales, void *out, moelora_stream_t stream);
+
 MOELORA_API const char *moelora_status_string(moelora_status status);
 
 /* ---------------------------------------------------------------------

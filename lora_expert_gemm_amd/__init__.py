@@ -43,6 +43,8 @@ F32, BF16, BF16_FP8W = 0, 1, 2
 DEVERR_EXPERT_ID, DEVERR_ADAPTER_ID = 1, 2
 FLAG_DETERMINISTIC, FLAG_DEBUG_CHECK_IDS = 1, 2
 FP8_SILU_MUL = 1
+ROUTE_SOFTMAX_ALL = 1
+FP4_SILU_MUL = 1
 N_STAGES = 6
 STAGES = ("route_align", "shrink_gate_up", "gate_up", "shrink_down", "down", "combine")
 
@@ -98,8 +100,18 @@ _lib.moelora_quantize_rows.argtypes = [_I32] * 3 + [_P, _I32, _P, _I32] + [_P] *
 _lib.moelora_quantize_weights.argtypes = [_I32] * 4 + [_P] * 6
 _lib.moelora_fp8_gemm.argtypes = [_I32] * 5 + [_U32] + [_P] * 7
 _lib.moelora_fp8_gemm_info.argtypes = [_I32] * 5 + [_U32, ctypes.c_char_p, ctypes.c_size_t]
+_lib.moelora_route.argtypes = [_I32] * 4 + [_U32] + [_P] * 5
+_lib.moelora_balance_loss_workspace.argtypes = [_I32] * 3 + [ctypes.POINTER(ctypes.c_size_t)]
+_lib.moelora_balance_loss.argtypes = [_I32] * 4 + [_P] * 7 + [ctypes.c_size_t, _P]
+_lib.moelora_route_backward.argtypes = [_I32] * 4 + [_U32] + [_P] * 9
+_lib.moelora_quantize_weights_fp4.argtypes = [_I32] * 4 + [_P] * 4
+_lib.moelora_pack_weights_fp4.argtypes = [_I32] * 3 + [_P] * 5
+_lib.moelora_dequantize_weights_fp4.argtypes = [_I32] * 4 + [_P] * 4
+_lib.moelora_fp4_gemm.argtypes = [_I32] * 5 + [_U32] + [_P] * 6
 for _n in ("dispatch_workspace", "dispatch", "dispatch_backward", "combine", "combine_backward",
-           "quantize_rows", "quantize_weights", "fp8_gemm", "fp8_gemm_info"):
+           "quantize_rows", "quantize_weights", "fp8_gemm", "fp8_gemm_info", "route",
+           "balance_loss_workspace", "balance_loss", "route_backward", "quantize_weights_fp4",
+           "pack_weights_fp4", "dequantize_weights_fp4", "fp4_gemm"):
     getattr(_lib, "moelora_" + _n).restype = ctypes.c_int
 
 
@@ -370,6 +382,97 @@ def moelora_fp8_gemm_info(n_rows, n_out, width, n_experts, out_dtype, flags=0):
     _check(_lib.moelora_fp8_gemm_info(n_rows, n_out, width, n_experts, out_dtype, flags, buf, len(buf)),
            "moelora_fp8_gemm_info")
     return buf.value.decode()
+
+
+def moelora_route(n_tokens, n_experts, top_k, dtype, flags, logits, token_mask, topk_ids, topk_w,
+                  stream=None):
+    st, dev = _where(stream)
+    R = n_tokens * top_k
+    _check(_lib.moelora_route(
+        n_tokens, n_experts, top_k, dtype, flags,
+        _buf(logits, n_tokens * n_experts, _dt(dtype), dev, "logits"),
+        _buf(token_mask, n_tokens, _BYTE, dev, "token_mask", True), _buf(topk_ids, R, _INT, dev, "topk_ids"),
+        _buf(topk_w, R, _FLT, dev, "topk_w"), st), "moelora_route")
+
+
+def moelora_balance_loss_workspace(n_tokens, n_experts, top_k):
+    """-> workspace bytes of moelora_balance_loss."""
+    n = ctypes.c_size_t()
+    _check(_lib.moelora_balance_loss_workspace(n_tokens, n_experts, top_k, ctypes.byref(n)),
+           "moelora_balance_loss_workspace")
+    return n.value
+
+
+def moelora_balance_loss(n_tokens, n_experts, top_k, dtype, logits, token_mask, topk_ids, counts,
+                         prob_sum, loss, workspace, workspace_bytes, stream=None):
+    st, dev = _where(stream)
+    _check(_lib.moelora_balance_loss(
+        n_tokens, n_experts, top_k, dtype, _buf(logits, n_tokens * n_experts, _dt(dtype), dev, "logits"),
+        _buf(token_mask, n_tokens, _BYTE, dev, "token_mask", True),
+        _buf(topk_ids, n_tokens * top_k, _INT, dev, "topk_ids"),
+        _buf(counts, n_experts + 1, _INT, dev, "counts"), _buf(prob_sum, n_experts, _FLT, dev, "prob_sum"),
+        _buf(loss, 2, _FLT, dev, "loss"),
+        _buf(workspace, workspace_bytes, _BYTE, dev, "workspace", True), workspace_bytes,
+        st), "moelora_balance_loss")
+
+
+def moelora_route_backward(n_tokens, n_experts, top_k, dtype, flags, logits, token_mask, topk_ids,
+                           topk_w, dtopk_w, counts, dloss, dlogits, stream=None):
+    st, dev = _where(stream)
+    R, n, dt = n_tokens * top_k, n_tokens * n_experts, _dt(dtype)
+    _check(_lib.moelora_route_backward(
+        n_tokens, n_experts, top_k, dtype, flags, _buf(logits, n, dt, dev, "logits"),
+        _buf(token_mask, n_tokens, _BYTE, dev, "token_mask", True),
+        _buf(topk_ids, R, _INT, dev, "topk_ids", dtopk_w is None),
+        _buf(topk_w, R, _FLT, dev, "topk_w", dtopk_w is None), _buf(dtopk_w, R, _FLT, dev, "dtopk_w", True),
+        _buf(counts, n_experts + 1, _INT, dev, "counts", True), _buf(dloss, 2, _FLT, dev, "dloss", True),
+        _buf(dlogits, n, dt, dev, "dlogits"), st), "moelora_route_backward")
+
+
+def _fp4_bytes(n_mats, rows, width):
+    """Bytes of the codes and of the scales of 4-bit weights."""
+    tiles, kb = n_mats * ((rows + 15) // 16), (width + 127) // 128
+    return tiles * kb * 1024, tiles * ((kb + 3) // 4) * 256
+
+
+def moelora_quantize_weights_fp4(n_mats, rows, width, dtype, w, codes, scales, stream=None):
+    st, dev = _where(stream)
+    nc, ns = _fp4_bytes(n_mats, rows, width)
+    _check(_lib.moelora_quantize_weights_fp4(
+        n_mats, rows, width, dtype, _buf(w, n_mats * rows * width, _dt(dtype), dev, "w"),
+        _buf(codes, nc, _BYTE, dev, "codes"), _buf(scales, ns, _BYTE, dev, "scales"), st),
+        "moelora_quantize_weights_fp4")
+
+
+def moelora_pack_weights_fp4(n_mats, rows, width, row_codes, row_scales, codes, scales, stream=None):
+    st, dev = _where(stream)
+    nc, ns = _fp4_bytes(n_mats, rows, width)
+    _check(_lib.moelora_pack_weights_fp4(
+        n_mats, rows, width, _buf(row_codes, n_mats * rows * ((width + 1) // 2), _BYTE, dev, "row_codes"),
+        _buf(row_scales, n_mats * rows * ((width + 31) // 32), _BYTE, dev, "row_scales"),
+        _buf(codes, nc, _BYTE, dev, "codes"), _buf(scales, ns, _BYTE, dev, "scales"), st),
+        "moelora_pack_weights_fp4")
+
+
+def moelora_dequantize_weights_fp4(n_mats, rows, width, dtype, codes, scales, w, stream=None):
+    st, dev = _where(stream)
+    nc, ns = _fp4_bytes(n_mats, rows, width)
+    _check(_lib.moelora_dequantize_weights_fp4(
+        n_mats, rows, width, dtype, _buf(codes, nc, _BYTE, dev, "codes"),
+        _buf(scales, ns, _BYTE, dev, "scales"), _buf(w, n_mats * rows * width, _dt(dtype), dev, "w"), st),
+        "moelora_dequantize_weights_fp4")
+
+
+def moelora_fp4_gemm(n_rows, n_out, width, n_experts, dtype, flags, x, expert_start, w_codes, w_scales,
+                     out, stream=None):
+    st, dev = _where(stream)
+    nc, ns = _fp4_bytes(n_experts * (2 if flags & FP4_SILU_MUL else 1), n_out, width)
+    dt = _dt(dtype)
+    _check(_lib.moelora_fp4_gemm(
+        n_rows, n_out, width, n_experts, dtype, flags, _buf(x, n_rows * width, dt, dev, "x"),
+        _buf(expert_start, n_experts + 1, _INT, dev, "expert_start", True),
+        _buf(w_codes, nc, _BYTE, dev, "w_codes"), _buf(w_scales, ns, _BYTE, dev, "w_scales"),
+        _buf(out, n_rows * n_out, dt, dev, "out"), st), "moelora_fp4_gemm")
 
 
 class Plan:

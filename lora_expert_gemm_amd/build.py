@@ -18,7 +18,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIB_DIR, "libmoelora.so")
 SOURCES = ["api.hip", "align.hip", "expert_gemm.hip", "tiled_gemm.hip",
-           "ops_api.hip", "token_order.hip", "block_fp8.hip", "fp8_gemm.hip"]
+           "ops_api.hip", "token_order.hip", "block_fp8.hip", "fp8_gemm.hip",
+           "router.hip", "fp4.hip", "fp4_gemm.hip"]
 ARCH = "gfx950"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

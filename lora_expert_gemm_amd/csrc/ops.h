@@ -1,6 +1,7 @@
 // Arguments and host-side launchers of the stand-alone operators: token
 // order (dispatch / combine and their gradients), block-of-128 E4M3
-// quantisation and the block-scaled product.
+// quantisation and the block-scaled product, the router with its losses, 4-bit
+// weights and their product.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -85,5 +86,59 @@ Fp8Choice choose_fp8_gemm(const Fp8GemmArgs &a, bool silu, bool bf16);
 hipError_t launch_fp8_gemm(const Fp8GemmArgs &a, bool silu, bool bf16, hipStream_t st);
 // With tl_resolve_only set: looks up every kernel launch_fp8_gemm can pick.
 hipError_t resolve_fp8_gemm(bool silu, bool bf16);
+
+// Router logits of T tokens over E experts, k picks each; mask null: every token.
+struct RouterArgs {
+  const void *logits;
+  const uint8_t *mask;
+  int T, E, k;
+};
+hipError_t launch_route(const RouterArgs &a, bool all, bool bf16, int *ids, float *w, hipStream_t st);
+
+struct BalanceOut {
+  int *counts;      // [E + 1]
+  float *prob_sum;  // [E]
+  float *loss;      // [2]
+};
+// Workgroups whose sums launch_balance keeps in its workspace (1: none there).
+constexpr int kBalanceChunks = 256;
+int balance_chunks(int T, int E);
+hipError_t launch_balance(const RouterArgs &a, bool bf16, const int *ids, const BalanceOut &o, void *ws,
+                          hipStream_t st);
+
+struct RouteGradArgs {
+  const int *ids;     // [T][k]
+  const float *w;     // [T][k]
+  const float *dw;    // [T][k], null: no gradient of the weights
+  const int *counts;  // [E + 1], null: none of the losses
+  const float *dloss; // [2]
+  void *dlogits;
+};
+hipError_t launch_route_backward(const RouterArgs &a, const RouteGradArgs &q, bool all, bool bf16,
+                                 hipStream_t st);
+
+// 4-bit weights: mats matrices of N rows x K, in tiles of 16 x 128 (fp4.h).
+struct Fp4WeightsArgs {
+  const void *src;            // weights, or row-major codes
+  const uint8_t *src_scales;  // row-major scales, with row-major codes
+  void *dst;                  // values, for the way back
+  uint8_t *codes, *scales;
+  int mats, N, K;
+  int NT, KB, KQ;  // tiles along N and K, fours of tiles along K
+};
+hipError_t launch_quantize_fp4(const Fp4WeightsArgs &a, bool bf16, hipStream_t st);
+hipError_t launch_pack_fp4(const Fp4WeightsArgs &a, hipStream_t st);
+hipError_t launch_dequantize_fp4(const Fp4WeightsArgs &a, bool bf16, hipStream_t st);
+
+struct Fp4GemmArgs {
+  const void *x;      // [R][K]
+  const int *start;   // [E + 1], null with E = 1: all rows
+  const uint8_t *w;   // [E][halves] matrices of codes
+  const uint8_t *ws;  // ... and of scales
+  void *out;          // [R][N]
+  int R, N, K, E;
+  int NT, KB, KQ;
+};
+hipError_t launch_fp4_gemm(const Fp4GemmArgs &a, bool silu, bool bf16, hipStream_t st);
 
 }  // namespace moelora

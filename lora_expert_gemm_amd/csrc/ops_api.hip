@@ -47,6 +47,20 @@ hipError_t resolve_all() {
     need(launch_quantize_rows(QuantRowsArgs{f, nullptr, fb, ff, 1, 1, 1, 1}, bf16, nullptr));
     need(launch_quantize_weights(QuantWeightsArgs{f, fb, nullptr, ff, nullptr, 1, 1, 1}, bf16, nullptr));
     for (int silu = 0; silu < 2; ++silu) need(resolve_fp8_gemm(silu, bf16));
+    for (int E : {16, 32, 64, 128, 256, 512, 1024}) {  // one of each of the router's forms
+      const RouterArgs r{f, nullptr, 1, E, 1};
+      for (int all = 0; all < 2; ++all) {
+        need(launch_route(r, all, bf16, fi, ff, nullptr));
+        need(launch_route_backward(r, RouteGradArgs{fi, ff, ff, fi, ff, f}, all, bf16, nullptr));
+      }
+      need(launch_balance(r, bf16, fi, BalanceOut{fi, ff, ff}, f, nullptr));
+    }
+    const Fp4WeightsArgs w{f, fb, f, fb, fb, 1, 1, 1, 1, 1, 1};
+    need(launch_quantize_fp4(w, bf16, nullptr));
+    need(launch_pack_fp4(w, nullptr));
+    need(launch_dequantize_fp4(w, bf16, nullptr));
+    for (int silu = 0; silu < 2; ++silu)
+      need(launch_fp4_gemm(Fp4GemmArgs{f, nullptr, fb, fb, f, 1, 1, 1, 1, 1, 1, 1}, silu, bf16, nullptr));
   }
   return e;
 }
@@ -102,6 +116,54 @@ moelora_status gemm_shape(int32_t n_rows, int32_t n_out, int32_t width, int32_t 
   a->NB = (n_out + 127) / 128;
   a->P = row_pitch8(width);
   return MOELORA_OK;
+}
+
+// Sizes of the router's operators; the pointers are left null.
+moelora_status router_shape(int32_t T, int32_t E, int32_t k, int32_t dtype, RouterArgs *a) {
+  if (T < 0) return MOELORA_ERR_INVALID_ARG;
+  if (E < 1 || E > kMaxE || k < 1 || k > kMaxK || k > E || (long long)T * k > kMaxRows ||
+      (dtype != MOELORA_F32 && dtype != MOELORA_BF16))
+    return MOELORA_ERR_UNSUPPORTED;
+  *a = RouterArgs{nullptr, nullptr, T, E, k};
+  return MOELORA_OK;
+}
+size_t balance_ws(const RouterArgs &a) {
+  const int c = balance_chunks(a.T, a.E);
+  return c > 1 ? (size_t)c * (2 * a.E + 2) * 4 : 0;
+}
+
+constexpr long long kMaxTileFours = 1ll << 26;  // (a launch holds fewer than 2^32 threads)
+// Sizes of 4-bit weights; the pointers are left null.
+moelora_status fp4_shape(int32_t mats, int32_t N, int32_t K, Fp4WeightsArgs *a) {
+  if (mats < 0) return MOELORA_ERR_INVALID_ARG;
+  if (mats > kMaxMats || N < 1 || N > kMaxOut || K < 1 || K > kMaxWidth) return MOELORA_ERR_UNSUPPORTED;
+  a->mats = mats;
+  a->N = N;
+  a->K = K;
+  a->NT = (N + 15) / 16;
+  a->KB = (K + 127) / 128;
+  a->KQ = (a->KB + 3) / 4;
+  return (long long)mats * a->NT * a->KQ < kMaxTileFours ? MOELORA_OK : MOELORA_ERR_UNSUPPORTED;
+}
+
+// Sizes of the product on 4-bit weights; the pointers are left null.
+moelora_status fp4_gemm_shape(int32_t n_rows, int32_t n_out, int32_t width, int32_t n_experts, int32_t dtype,
+                              uint32_t flags, Fp4GemmArgs *a) {
+  if (n_rows < 0) return MOELORA_ERR_INVALID_ARG;
+  if (n_rows > kMaxRows || n_experts < 1 || n_experts > kMaxE || (flags & ~MOELORA_FP4_SILU_MUL) ||
+      (dtype != MOELORA_F32 && dtype != MOELORA_BF16))
+    return MOELORA_ERR_UNSUPPORTED;
+  Fp4WeightsArgs w{};
+  const moelora_status st = fp4_shape(n_experts * (flags & MOELORA_FP4_SILU_MUL ? 2 : 1), n_out, width, &w);
+  *a = Fp4GemmArgs{};
+  a->R = n_rows;
+  a->N = n_out;
+  a->K = width;
+  a->E = n_experts;
+  a->NT = w.NT;
+  a->KB = w.KB;
+  a->KQ = w.KQ;
+  return st;
 }
 
 size_t dispatch_ws(const OrderShape &s) { return dispatch_counts(s.R, s.E) * (size_t)s.E * 4; }
@@ -265,6 +327,137 @@ moelora_status moelora_fp8_gemm_info(int32_t n_rows, int32_t n_out, int32_t widt
   }
   snprintf(buf, buf_len, "kernel=%s groups=%d", name, c.groups);
   return MOELORA_OK;
+}
+
+moelora_status moelora_route(int32_t n_tokens, int32_t n_experts, int32_t top_k, int32_t dtype, uint32_t flags,
+                             const void *logits, const uint8_t *token_mask, int32_t *topk_ids, float *topk_w,
+                             moelora_stream_t stream) {
+  RouterArgs a;
+  moelora_status st = router_shape(n_tokens, n_experts, top_k, dtype, &a);
+  if (st != MOELORA_OK) return st;
+  if (flags & ~MOELORA_ROUTE_SOFTMAX_ALL) return MOELORA_ERR_UNSUPPORTED;
+  if (n_tokens == 0) return MOELORA_OK;
+  if (!ok16(logits) || !opt16(token_mask) || !ok16(topk_ids) || !ok16(topk_w)) return MOELORA_ERR_INVALID_ARG;
+  if ((st = ready()) != MOELORA_OK) return st;
+  a.logits = logits;
+  a.mask = token_mask;
+  return from_hip(launch_route(a, flags & MOELORA_ROUTE_SOFTMAX_ALL, dtype == MOELORA_BF16, topk_ids, topk_w,
+                               reinterpret_cast<hipStream_t>(stream)));
+}
+
+moelora_status moelora_balance_loss_workspace(int32_t n_tokens, int32_t n_experts, int32_t top_k,
+                                              size_t *workspace_bytes) {
+  if (!workspace_bytes) return MOELORA_ERR_INVALID_ARG;
+  RouterArgs a;
+  const moelora_status st = router_shape(n_tokens, n_experts, top_k, MOELORA_F32, &a);
+  if (st == MOELORA_OK) *workspace_bytes = balance_ws(a);
+  return st;
+}
+
+moelora_status moelora_balance_loss(int32_t n_tokens, int32_t n_experts, int32_t top_k, int32_t dtype,
+                                    const void *logits, const uint8_t *token_mask, const int32_t *topk_ids,
+                                    int32_t *counts, float *prob_sum, float *loss, void *workspace,
+                                    size_t workspace_bytes, moelora_stream_t stream) {
+  RouterArgs a;
+  moelora_status st = router_shape(n_tokens, n_experts, top_k, dtype, &a);
+  if (st != MOELORA_OK) return st;
+  if (!ok16(counts) || !ok16(prob_sum) || !ok16(loss)) return MOELORA_ERR_INVALID_ARG;
+  if (n_tokens > 0 && (!ok16(logits) || !opt16(token_mask) || !ok16(topk_ids))) return MOELORA_ERR_INVALID_ARG;
+  const size_t need = balance_ws(a);
+  if (need > 0 && !ok16(workspace)) return MOELORA_ERR_INVALID_ARG;
+  if (workspace_bytes < need) return MOELORA_ERR_WORKSPACE;
+  if ((st = ready()) != MOELORA_OK) return st;
+  a.logits = logits;
+  a.mask = token_mask;
+  return from_hip(launch_balance(a, dtype == MOELORA_BF16, topk_ids, BalanceOut{counts, prob_sum, loss}, workspace,
+                                 reinterpret_cast<hipStream_t>(stream)));
+}
+
+moelora_status moelora_route_backward(int32_t n_tokens, int32_t n_experts, int32_t top_k, int32_t dtype,
+                                      uint32_t flags, const void *logits, const uint8_t *token_mask,
+                                      const int32_t *topk_ids, const float *topk_w, const float *dtopk_w,
+                                      const int32_t *counts, const float *dloss, void *dlogits,
+                                      moelora_stream_t stream) {
+  RouterArgs a;
+  moelora_status st = router_shape(n_tokens, n_experts, top_k, dtype, &a);
+  if (st != MOELORA_OK) return st;
+  if (flags & ~MOELORA_ROUTE_SOFTMAX_ALL) return MOELORA_ERR_UNSUPPORTED;
+  if (n_tokens == 0) return MOELORA_OK;
+  if (!ok16(logits) || !opt16(token_mask) || !opt16(topk_ids) || !opt16(topk_w) || !opt16(dtopk_w) ||
+      !opt16(counts) || !opt16(dloss) || !ok16(dlogits) || (!dtopk_w && !counts) || !counts != !dloss ||
+      (dtopk_w && (!topk_ids || !topk_w)))
+    return MOELORA_ERR_INVALID_ARG;
+  if ((st = ready()) != MOELORA_OK) return st;
+  a.logits = logits;
+  a.mask = token_mask;
+  return from_hip(launch_route_backward(a, RouteGradArgs{topk_ids, topk_w, dtopk_w, counts, dloss, dlogits},
+                                        flags & MOELORA_ROUTE_SOFTMAX_ALL, dtype == MOELORA_BF16,
+                                        reinterpret_cast<hipStream_t>(stream)));
+}
+
+moelora_status moelora_quantize_weights_fp4(int32_t n_mats, int32_t rows, int32_t width, int32_t dtype,
+                                            const void *w, void *codes, void *scales, moelora_stream_t stream) {
+  Fp4WeightsArgs a{};
+  moelora_status st = fp4_shape(n_mats, rows, width, &a);
+  if (st != MOELORA_OK) return st;
+  if (dtype != MOELORA_F32 && dtype != MOELORA_BF16) return MOELORA_ERR_UNSUPPORTED;
+  if (n_mats == 0) return MOELORA_OK;
+  if (!ok16(w) || !ok16(codes) || !ok16(scales)) return MOELORA_ERR_INVALID_ARG;
+  if ((st = ready()) != MOELORA_OK) return st;
+  a.src = w;
+  a.codes = static_cast<uint8_t *>(codes);
+  a.scales = static_cast<uint8_t *>(scales);
+  return from_hip(launch_quantize_fp4(a, dtype == MOELORA_BF16, reinterpret_cast<hipStream_t>(stream)));
+}
+
+moelora_status moelora_pack_weights_fp4(int32_t n_mats, int32_t rows, int32_t width, const void *row_codes,
+                                        const void *row_scales, void *codes, void *scales,
+                                        moelora_stream_t stream) {
+  Fp4WeightsArgs a{};
+  moelora_status st = fp4_shape(n_mats, rows, width, &a);
+  if (st != MOELORA_OK || n_mats == 0) return st;
+  if (!ok16(row_codes) || !ok16(row_scales) || !ok16(codes) || !ok16(scales)) return MOELORA_ERR_INVALID_ARG;
+  if ((st = ready()) != MOELORA_OK) return st;
+  a.src = row_codes;
+  a.src_scales = static_cast<const uint8_t *>(row_scales);
+  a.codes = static_cast<uint8_t *>(codes);
+  a.scales = static_cast<uint8_t *>(scales);
+  return from_hip(launch_pack_fp4(a, reinterpret_cast<hipStream_t>(stream)));
+}
+
+moelora_status moelora_dequantize_weights_fp4(int32_t n_mats, int32_t rows, int32_t width, int32_t dtype,
+                                              const void *codes, const void *scales, void *w,
+                                              moelora_stream_t stream) {
+  Fp4WeightsArgs a{};
+  moelora_status st = fp4_shape(n_mats, rows, width, &a);
+  if (st != MOELORA_OK) return st;
+  if (dtype != MOELORA_F32 && dtype != MOELORA_BF16) return MOELORA_ERR_UNSUPPORTED;
+  if (n_mats == 0) return MOELORA_OK;
+  if (!ok16(w) || !ok16(codes) || !ok16(scales)) return MOELORA_ERR_INVALID_ARG;
+  if ((st = ready()) != MOELORA_OK) return st;
+  a.dst = w;
+  a.codes = static_cast<uint8_t *>(const_cast<void *>(codes));  // (read only on this way)
+  a.scales = static_cast<uint8_t *>(const_cast<void *>(scales));
+  return from_hip(launch_dequantize_fp4(a, dtype == MOELORA_BF16, reinterpret_cast<hipStream_t>(stream)));
+}
+
+moelora_status moelora_fp4_gemm(int32_t n_rows, int32_t n_out, int32_t width, int32_t n_experts, int32_t dtype,
+                                uint32_t flags, const void *x, const int32_t *expert_start, const void *w_codes,
+                                const void *w_scales, void *out, moelora_stream_t stream) {
+  Fp4GemmArgs a;
+  moelora_status st = fp4_gemm_shape(n_rows, n_out, width, n_experts, dtype, flags, &a);
+  if (st != MOELORA_OK || n_rows == 0) return st;
+  if (!ok16(x) || !opt16(expert_start) || !ok16(w_codes) || !ok16(w_scales) || !ok16(out) ||
+      (!expert_start && n_experts != 1))
+    return MOELORA_ERR_INVALID_ARG;
+  if ((st = ready()) != MOELORA_OK) return st;
+  a.x = x;
+  a.start = expert_start;
+  a.w = static_cast<const uint8_t *>(w_codes);
+  a.ws = static_cast<const uint8_t *>(w_scales);
+  a.out = out;
+  return from_hip(launch_fp4_gemm(a, flags & MOELORA_FP4_SILU_MUL, dtype == MOELORA_BF16,
+                                  reinterpret_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"
