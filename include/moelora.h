@@ -459,6 +459,12 @@ MOELORA_API moelora_status moelora_fp4_gemm(int32_t n_rows, int32_t n_out, int32
                                const int32_t *expert_start, const void *w_codes,
                                const void *w_scales, void *out, moelora_stream_t stream);
 
+/* A one-line description of the kernel that a product of these sizes takes
+ * (for logs; host only): NUL-terminated, truncated to buf_len. */
+MOELORA_API moelora_status moelora_fp4_gemm_info(int32_t n_rows, int32_t n_out, int32_t width,
+                               int32_t n_experts, int32_t dtype, uint32_t flags,
+                               char *buf, size_t buf_len);
+
 MOELORA_API const char *moelora_status_string(moelora_status status);
 
 /* ---------------------------------------------------------------------

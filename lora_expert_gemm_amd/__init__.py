@@ -108,10 +108,11 @@ _lib.moelora_quantize_weights_fp4.argtypes = [_I32] * 4 + [_P] * 4
 _lib.moelora_pack_weights_fp4.argtypes = [_I32] * 3 + [_P] * 5
 _lib.moelora_dequantize_weights_fp4.argtypes = [_I32] * 4 + [_P] * 4
 _lib.moelora_fp4_gemm.argtypes = [_I32] * 5 + [_U32] + [_P] * 6
+_lib.moelora_fp4_gemm_info.argtypes = [_I32] * 5 + [_U32, ctypes.c_char_p, ctypes.c_size_t]
 for _n in ("dispatch_workspace", "dispatch", "dispatch_backward", "combine", "combine_backward",
            "quantize_rows", "quantize_weights", "fp8_gemm", "fp8_gemm_info", "route",
            "balance_loss_workspace", "balance_loss", "route_backward", "quantize_weights_fp4",
-           "pack_weights_fp4", "dequantize_weights_fp4", "fp4_gemm"):
+           "pack_weights_fp4", "dequantize_weights_fp4", "fp4_gemm", "fp4_gemm_info"):
     getattr(_lib, "moelora_" + _n).restype = ctypes.c_int
 
 
@@ -473,6 +474,14 @@ def moelora_fp4_gemm(n_rows, n_out, width, n_experts, dtype, flags, x, expert_st
         _buf(expert_start, n_experts + 1, _INT, dev, "expert_start", True),
         _buf(w_codes, nc, _BYTE, dev, "w_codes"), _buf(w_scales, ns, _BYTE, dev, "w_scales"),
         _buf(out, n_rows * n_out, dt, dev, "out"), st), "moelora_fp4_gemm")
+
+
+def moelora_fp4_gemm_info(n_rows, n_out, width, n_experts, dtype, flags=0):
+    """-> one line on the kernel that such a product takes."""
+    buf = ctypes.create_string_buffer(128)
+    _check(_lib.moelora_fp4_gemm_info(n_rows, n_out, width, n_experts, dtype, flags, buf, len(buf)),
+           "moelora_fp4_gemm_info")
+    return buf.value.decode()
 
 
 class Plan:

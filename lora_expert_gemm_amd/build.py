@@ -34,7 +34,7 @@ FLAGS = [
 # Sources whose GEMM kernels wait on counts of their own vector-memory loads
 # (s_waitcnt vmcnt with a fixed immediate): a scratch spill reload is a
 # vector load too, so every kernel of these must use no scratch memory.
-COUNTED_WAITS = ("expert_gemm.hip", "tiled_gemm.hip", "fp8_gemm.hip")
+COUNTED_WAITS = ("expert_gemm.hip", "tiled_gemm.hip", "fp8_gemm.hip", "fp4_gemm.hip")
 # The device assembly of the streaming GEMMs is kept for the CPU test that
 # checks the compiled weight-ring loops against their wait counts.
 ASM_SOURCES = ("expert_gemm.hip",)

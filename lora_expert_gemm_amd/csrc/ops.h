@@ -139,6 +139,20 @@ struct Fp4GemmArgs {
   int R, N, K, E;
   int NT, KB, KQ;
 };
+// Which kernel a product takes: streamed, with 1 or 2 groups of 16 rows at a time
+// and `groups` workgroups to share an expert's groups, or tiled, with weight tiles
+// x token tiles of 16 a wave, the tokens straight into LDS (bf16 rows of whole 16
+// bytes) or through registers; Once: the weights go past the caches.
+enum class Fp4Kernel { kStream1, kStream2, kTile2x2Once, kTile2x4, kTile4x4, kTile4x8, kRegs2x2, kRegs4x4 };
+constexpr int kFp4Kernels = 8;
+constexpr bool fp4_needs_bf16(Fp4Kernel k) { return k >= Fp4Kernel::kTile2x2Once && k <= Fp4Kernel::kTile4x8; }
+struct Fp4Choice {
+  Fp4Kernel kernel;
+  int groups;
+};
+Fp4Choice choose_fp4_gemm(const Fp4GemmArgs &a, bool silu, bool bf16);
 hipError_t launch_fp4_gemm(const Fp4GemmArgs &a, bool silu, bool bf16, hipStream_t st);
+// With tl_resolve_only set: looks up every kernel launch_fp4_gemm can pick.
+hipError_t resolve_fp4_gemm(bool silu, bool bf16);
 
 }  // namespace moelora

@@ -59,8 +59,7 @@ hipError_t resolve_all() {
     need(launch_quantize_fp4(w, bf16, nullptr));
     need(launch_pack_fp4(w, nullptr));
     need(launch_dequantize_fp4(w, bf16, nullptr));
-    for (int silu = 0; silu < 2; ++silu)
-      need(launch_fp4_gemm(Fp4GemmArgs{f, nullptr, fb, fb, f, 1, 1, 1, 1, 1, 1, 1}, silu, bf16, nullptr));
+    for (int silu = 0; silu < 2; ++silu) need(resolve_fp4_gemm(silu, bf16));
   }
   return e;
 }
@@ -458,6 +457,23 @@ moelora_status moelora_fp4_gemm(int32_t n_rows, int32_t n_out, int32_t width, in
   a.out = out;
   return from_hip(launch_fp4_gemm(a, flags & MOELORA_FP4_SILU_MUL, dtype == MOELORA_BF16,
                                   reinterpret_cast<hipStream_t>(stream)));
+}
+
+moelora_status moelora_fp4_gemm_info(int32_t n_rows, int32_t n_out, int32_t width, int32_t n_experts,
+                                     int32_t dtype, uint32_t flags, char *buf, size_t buf_len) {
+  Fp4GemmArgs a;
+  const moelora_status st = fp4_gemm_shape(n_rows, n_out, width, n_experts, dtype, flags, &a);
+  if (st != MOELORA_OK) return st;
+  if (!buf || buf_len == 0) return MOELORA_ERR_INVALID_ARG;
+  if (n_rows == 0) {
+    snprintf(buf, buf_len, "kernel=none");
+    return MOELORA_OK;
+  }
+  static const char *const names[kFp4Kernels] = {"stream1", "stream2", "tile2x2_once", "tile2x4",
+                                                 "tile4x4", "tile4x8", "regs2x2", "regs4x4"};
+  const Fp4Choice c = choose_fp4_gemm(a, flags & MOELORA_FP4_SILU_MUL, dtype == MOELORA_BF16);
+  snprintf(buf, buf_len, "kernel=%s groups=%d", names[(int)c.kernel], c.groups);
+  return MOELORA_OK;
 }
 
 }  // extern "C"
