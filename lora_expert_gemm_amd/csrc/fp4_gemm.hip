@@ -57,22 +57,82 @@ template <> struct Parts<float> {
   }
 };
 
-// Elements c .. c + 7 of a row of K as they are stored, zeros past K.  Whole
-// ones are 16-byte loads, which need no more than 2-byte alignment here.
+// v shifted right by 0 <= n <= 16 bytes.
+__device__ __forceinline__ u32x4_t shift_right(u32x4_t v, int n) {
+  typedef unsigned long long u64;
+  u64 lo = (u64)v[1] << 32 | v[0], hi = (u64)v[3] << 32 | v[2];
+  const int bits = 8 * n & 63;
+  if (n >= 8) lo = hi, hi = 0;
+  if (n >= 16) lo = 0;
+  lo = lo >> bits | (hi << 1) << (63 - bits);
+  hi >>= bits;
+  return u32x4_t{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+}
+
+// Elements c .. c + 7 of the row of K (16 bytes or more) that starts `row` elements behind `base`, as
+// 16-byte loads, which need no more than 2-byte alignment here.  One that would
+// pass the row's end is moved back to end with it; fix8 shifts it to its place,
+// zeros behind, where the values are needed, so that the load itself need not be
+// waited for.
+template <typename DT> constexpr int kPerLoad = 16 / (int)sizeof(DT);
 template <typename DT>
-__device__ __forceinline__ void load8(const DT *row, int c, int K, u32x4_t *v) {
+__device__ __forceinline__ void load8(const DT *base, uint32_t row, int c, int K, u32x4_t *v) {
   typedef u32x4_t mem __attribute__((aligned(2)));
-  constexpr int n = Parts<DT>::kLoads, per = 16 / sizeof(DT);
-  if (c + 8 <= K) {
+  constexpr int per = kPerLoad<DT>;
 #pragma unroll
-    for (int i = 0; i < n; ++i) v[i] = *reinterpret_cast<const mem *>(row + c + per * i);
-  } else {
+  for (int i = 0; i < Parts<DT>::kLoads; ++i) {
+    const int k = c + per * i;
+    const uint32_t at = (row + min(k, K - per)) * (uint32_t)sizeof(DT);
+    v[i] = *reinterpret_cast<const mem *>(reinterpret_cast<const char *>(base) + at);
+  }
+}
+template <typename DT> __device__ __forceinline__ void fix8(int c, int K, u32x4_t *v) {
+  constexpr int per = kPerLoad<DT>;
 #pragma unroll
-    for (int i = 0; i < n; ++i) {
-      Chunk<DT> e;
+  for (int i = 0; i < Parts<DT>::kLoads; ++i)
+    v[i] = shift_right(v[i], max(0, min(c + per * i - (K - per), per)) * (int)sizeof(DT));
+}
+
+// A wave's weights: WH neighbouring rows of tiles in each of HV matrices.
+template <int HV, int WH> struct TileRows {
+  const uint8_t *codes[HV], *scales[HV];
+  uint32_t at[WH], sat[WH];  // a lane's place in each row of tiles
+  int bytes, sbytes;         // of the rows that exist
+
+  __device__ __forceinline__ TileRows(const Fp4GemmArgs &a, int e, int t0, int lane) {
+    const int n = max(0, min(WH, a.NT - t0));
+    bytes = n * a.KB * kTileBytes, sbytes = n * a.KQ * kScaleBytes;
 #pragma unroll
-      for (int j = 0; j < per; ++j) e.v[j] = c + per * i + j < K ? row[c + per * i + j] : DT(0);
-      v[i] = __builtin_bit_cast(u32x4_t, e);
+    for (int h = 0; h < HV; ++h) {
+      const size_t row = ((size_t)e * HV + h) * a.NT + (n ? t0 : 0);
+      codes[h] = a.w + row * a.KB * kTileBytes, scales[h] = a.ws + row * a.KQ * kScaleBytes;
+    }
+#pragma unroll
+    for (int i = 0; i < WH; ++i) {
+      at[i] = i * a.KB * kTileBytes + lane * 16, sat[i] = i * a.KQ * kScaleBytes + lane * 4;
+    }
+  }
+};
+// A wave's tiles of slab b: a lane's 32 codes, and the scales of its groups in
+// slabs b / 4 * 4 .. + 3.  Rows that do not exist, and slabs past the last, lie
+// past their buffer resource's end: they fetch nothing and give zeros.
+template <int A> struct Weights {
+  u32x4_t c[A];
+  uint32_t s[A];
+};
+template <bool ONCE, int HV, int WH>
+__device__ __forceinline__ void load_weights(Weights<HV * WH> &w, const TileRows<HV, WH> &r, int KB, int b) {
+#pragma unroll
+  for (int h = 0; h < HV; ++h) {
+    const __amdgpu_buffer_rsrc_t codes = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint8_t *>(r.codes[h]), (short)0, b < KB ? r.bytes : 0, kBufferWord3);
+    const __amdgpu_buffer_rsrc_t scales = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint8_t *>(r.scales[h]), (short)0, b < KB ? r.sbytes : 0, kBufferWord3);
+#pragma unroll
+    for (int i = 0; i < WH; ++i) {
+      w.c[h * WH + i] =
+          __builtin_amdgcn_raw_buffer_load_b128(codes, r.at[i], b * kTileBytes, ONCE ? kCpolNonTemporal : 0);
+      w.s[h * WH + i] = __builtin_amdgcn_raw_buffer_load_b32(scales, r.sat[i], b / 4 * kScaleBytes, 0);
     }
   }
 }
@@ -80,88 +140,78 @@ __device__ __forceinline__ void load8(const DT *row, int c, int K, u32x4_t *v) {
 // ---------------------------------------------------------------- few rows
 //
 // A workgroup owns NT tiles of 16 weight rows (of each half) of one expert and
-// up to 16 TG of its tokens at a time (every gridDim.z-th group); its four waves take every
-// fourth tile along the contraction and add their sums through LDS in wave
-// order, so that a narrow product still fills the chip.  Weights go from memory
-// straight into registers, 1 KB a load.
-constexpr int kSWaves = 4;
-constexpr int kSThreads = kSWaves * kWave;
-
-template <int NT, int TG, bool SILU, typename DT>
-__global__ __launch_bounds__(kSThreads) void k_fp4_stream(Fp4GemmArgs a) {
+// up to 16 of its tokens at a time (every gridDim.z-th group); its W waves take every
+// W-th tile along the contraction, one ahead, and add their sums through LDS in
+// wave order, so that a narrow product still fills the chip.  Weights go from
+// memory straight into registers, 1 KB a load, tokens too.
+template <int NT, int W, bool ONCE, bool SILU, typename DT>
+__global__ __launch_bounds__(W * kWave) void k_fp4_stream(Fp4GemmArgs a) {
   constexpr int HV = SILU ? 2 : 1, A = HV * NT, XL = Parts<DT>::kLoads;
-  __shared__ f32x4_t red[kSWaves][A * TG][kWave];
+  __shared__ f32x4_t red[W][A][kWave];
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int l16 = lane & 15, g = lane >> 4;
   int e, lo, hi;
   if (!find_expert(a, blockIdx.y, e, lo, hi)) return;
-  const int KB = a.KB, t0 = blockIdx.x * NT;
-  const uint8_t *wp[A], *sp[A];
+  e = __builtin_amdgcn_readfirstlane(e);
+  const int KB = a.KB, K = a.K, t0 = blockIdx.x * NT;
+  const TileRows<HV, NT> tr(a, e, t0, lane);
+  for (int m0 = lo + blockIdx.z * 16; m0 < hi; m0 += gridDim.z * 16) {
+    f32x4_t acc[A];
 #pragma unroll
-  for (int i = 0; i < A; ++i) {
-    // (tiles past the last repeat it and are dropped)
-    const size_t tile = ((size_t)e * HV + i / NT) * a.NT + min(t0 + i % NT, a.NT - 1);
-    wp[i] = a.w + tile * KB * kTileBytes + lane * 16;
-    sp[i] = a.ws + tile * a.KQ * kScaleBytes + lane * 4;
-  }
-  for (int m0 = lo + blockIdx.z * 16 * TG; m0 < hi; m0 += gridDim.z * 16 * TG) {
-    f32x4_t acc[A][TG];
+    for (int i = 0; i < A; ++i) acc[i] = f32x4_t{0, 0, 0, 0};
+    const DT *const xrows = static_cast<const DT *>(a.x) + (size_t)m0 * K;
+    const uint32_t row = (uint32_t)min(l16, hi - m0 - 1) * K;  // (rows past the last repeat it and are dropped)
+    struct Slab {
+      Weights<A> w;
+      u32x4_t x[4][XL];
+    };
+    auto load = [&](Slab &v, int b) {
+      load_weights<ONCE, HV, NT>(v.w, tr, KB, b);
 #pragma unroll
-    for (int i = 0; i < A; ++i)
+      for (int c = 0; c < 4; ++c) load8<DT>(xrows, row, b * kTileCols + g * kGroup + 8 * c, K, v.x[c]);
+    };
+    static_assert(W % 4 == 0, "a wave's slabs have one place in the scales' fours");
+    Slab v;
+    load(v, wave);
+    for (int b = wave; b < KB; b += W) {
+      if ((b + 1) * kTileCols > K) {
 #pragma unroll
-      for (int t = 0; t < TG; ++t) acc[i][t] = f32x4_t{0, 0, 0, 0};
-    const DT *xp[TG];
-#pragma unroll
-    for (int t = 0; t < TG; ++t)  // (rows past the last repeat it and are dropped)
-      xp[t] = static_cast<const DT *>(a.x) + (size_t)min(m0 + 16 * t + l16, hi - 1) * a.K;
-    for (int b = wave; b < KB; b += kSWaves) {
-      u32x4_t w[A];
+        for (int c = 0; c < 4; ++c) fix8<DT>(b * kTileCols + g * kGroup + 8 * c, K, v.x[c]);
+      }
       float s[A];
 #pragma unroll
-      for (int i = 0; i < A; ++i) {
-        w[i] = *reinterpret_cast<const u32x4_t *>(wp[i] + (size_t)b * kTileBytes);
-        const uint32_t four = *reinterpret_cast<const uint32_t *>(sp[i] + (size_t)(b / 4) * kScaleBytes);
-        s[i] = scale_of_code(four >> 8 * (b % 4) & 255u);
+      for (int i = 0; i < A; ++i) s[i] = scale_of_code(v.w.s[i] >> 8 * (wave % 4) & 255u);  // (b % 4 is wave % 4)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        u32x4_t wv[A];
+#pragma unroll
+        for (int i = 0; i < A; ++i) wv[i] = e2m1x8_to_bf16(v.w.c[i][c], s[i]);
+        const Parts<DT> x = Parts<DT>::of(v.x[c]);
+#pragma unroll
+        for (int q = 0; q < Parts<DT>::kParts; ++q)
+#pragma unroll
+          for (int i = 0; i < A; ++i) Mma<uint16_t>::step(acc[i], wv[i], x.p[q]);
       }
-#pragma unroll
-      for (int t = 0; t < TG; ++t) {
-        u32x4_t v[4][XL];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) load8<DT>(xp[t], b * kTileCols + g * kGroup + 8 * c, a.K, v[c]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const Parts<DT> x = Parts<DT>::of(v[c]);
-#pragma unroll
-          for (int i = 0; i < A; ++i) {
-            const u32x4_t wv = e2m1x8_to_bf16(w[i][c], s[i]);
-#pragma unroll
-            for (int p = 0; p < Parts<DT>::kParts; ++p) Mma<uint16_t>::step(acc[i][t], wv, x.p[p]);
-          }
-        }
-      }
+      load(v, b + W);
     }
 #pragma unroll
-    for (int i = 0; i < A; ++i)
-#pragma unroll
-      for (int t = 0; t < TG; ++t) red[wave][i * TG + t][lane] = acc[i][t];
+    for (int i = 0; i < A; ++i) red[wave][i][lane] = acc[i];
     __syncthreads();
-    // one wave per (tile, token group): the four waves' sums in wave order
-    for (int q = wave; q < NT * TG; q += kSWaves) {
-      const int i = q / TG, t = q % TG;
+    // one wave per tile: the waves' sums in wave order
+    for (int i = wave; i < NT; i += W) {
       f32x4_t v[HV];
 #pragma unroll
       for (int h = 0; h < HV; ++h) {
-        const int at = (h * NT + i) * TG + t;
-        v[h] = red[0][at][lane];
+        v[h] = red[0][h * NT + i][lane];
 #pragma unroll
-        for (int w = 1; w < kSWaves; ++w) {
-          const f32x4_t o = red[w][at][lane];
+        for (int w = 1; w < W; ++w) {
+          const f32x4_t o = red[w][h * NT + i][lane];
 #pragma unroll
           for (int c = 0; c < 4; ++c) v[h][c] += o[c];
         }
       }
-      const int m = m0 + 16 * t + l16, n = (t0 + i) * kTileRows + 4 * g;
+      const int m = m0 + l16, n = (t0 + i) * kTileRows + 4 * g;
       if (m < hi && n < a.N) {
         float o[4];
 #pragma unroll
@@ -175,16 +225,18 @@ __global__ __launch_bounds__(kSThreads) void k_fp4_stream(Fp4GemmArgs a) {
 
 // --------------------------------------------------------------- many rows
 //
-// 16 TT token rows x 64 WT weight rows (SILU: half gate, half up) a workgroup
-// of 4 waves; a wave owns WT weight tiles against all the tokens.  Slabs of 128
-// columns: the tokens into LDS, where the waves share them, the weights into
-// registers of the wave that uses them, one tile a load, a slab ahead.
+// 16 TT token rows x 64 WT weight rows (SILU: half gate, half up) a workgroup;
+// KS groups of 4 waves take every KS-th slab of 128 columns each and add their
+// sums through LDS in the end, in their order.  A wave owns WT weight tiles against all the
+// tokens.  Per slab and group: the tokens into one of two LDS stages, where the waves
+// share them, the weights, a slab ahead, into registers of the wave that uses them, one tile a
+// load; one barrier.
 //
-// DMA: bf16 rows of whole 16-byte chunks go straight into two LDS stages, one
-// slab ahead, with one barrier a slab; rows past the expert's last and chunks past
-// K lie past the buffer resource's end, so their loads fetch nothing and give
-// zeros.  Otherwise (float32 rows, in their three parts; bf16 rows of odd length) they pass
-// through registers into one stage, between two barriers.
+// DMA: bf16 rows of whole 16-byte chunks go straight into LDS, a slab ahead;
+// rows past the expert's last and chunks past K lie past the buffer resource's
+// end, so their loads fetch nothing and give zeros.  Otherwise (float32 rows, in
+// their three parts; bf16 rows of any length) they pass through registers, a slab
+// ahead of their stage.
 constexpr int kGWaves = 4, kGThreads = kGWaves * kWave;
 
 // LDS byte offset of 16-byte chunk q of a 256-byte row: 16 consecutive rows read
@@ -199,84 +251,63 @@ __device__ __forceinline__ void dma16(const void *base, int bytes, unsigned char
   __builtin_amdgcn_raw_ptr_buffer_load_lds(res, (__attribute__((address_space(3))) void *)lds, 16, voff, soff, 0, 0);
 }
 
-template <int WT, int TT, bool ONCE, bool DMA, bool SILU, typename DT>
-__global__ __launch_bounds__(kGThreads, 2) void k_fp4_tiled(Fp4GemmArgs a, int ncols) {
+template <int WT, int TT, int KS, bool ONCE, bool DMA, bool SILU, typename DT>
+__global__ __launch_bounds__(KS * kGThreads, KS > 1 || WT * TT <= 4 ? 4 : WT * TT <= 8 || DMA ? 3 : 2) void k_fp4_tiled(
+    Fp4GemmArgs a, int ncols) {
   extern __shared__ __align__(16) unsigned char smem[];
   typedef Parts<DT> P;
   constexpr int HV = SILU ? 2 : 1, WH = WT / HV;  // weight tiles of a half
   constexpr int GM = 16 * TT, PLANE = GM * 256, STAGE = PLANE * P::kParts;
   static_assert(!DMA || sizeof(DT) == 2, "");
-  const int tid = threadIdx.x, lane = tid & (kWave - 1);
+  const int tid = threadIdx.x % kGThreads, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int kg = __builtin_amdgcn_readfirstlane(threadIdx.x / kGThreads);
   const int l16 = lane & 15, g = lane >> 4;
   const RowTile rt = find_tile(a, GM, ncols, blockIdx.x);
   if (rt.e < 0) return;
   const int rows = min(GM, rt.hi - rt.m0), KB = a.KB, K = a.K;
   const int t0 = (rt.nt * kGWaves + wave) * WH;  // the wave's first weight tile, in each half
-  const uint8_t *wp[WT], *sp[WT];
-#pragma unroll
-  for (int i = 0; i < WT; ++i) {
-    // (tiles past the last repeat it and are dropped)
-    const size_t tile = ((size_t)rt.e * HV + i / WH) * a.NT + min(t0 + i % WH, a.NT - 1);
-    wp[i] = a.w + tile * KB * kTileBytes;
-    sp[i] = a.ws + tile * a.KQ * kScaleBytes;
-  }
-  struct Weights {
-    u32x4_t c[WT];
-    uint32_t s[WT];
-  };
-  auto load_w = [&](Weights &w, int b) {
-    b = min(b, KB - 1);
-#pragma unroll
-    for (int i = 0; i < WT; ++i) {
-      const u32x4_t *p = reinterpret_cast<const u32x4_t *>(wp[i] + (size_t)b * kTileBytes) + lane;
-      w.c[i] = ONCE ? __builtin_nontemporal_load(p) : *p;
-      w.s[i] = reinterpret_cast<const uint32_t *>(sp[i] + (size_t)(b / 4) * kScaleBytes)[lane];
-    }
-  };
-
-  // ---- tokens
-  constexpr int XD = GM / 4 / kGWaves;  // DMA loads a wave and slab, 4 rows each
-  uint32_t xoff[DMA ? XD : 1], xtail[DMA ? XD : 1];
-  if constexpr (DMA) {
-#pragma unroll
-    for (int j = 0; j < XD; ++j) {
-      const int r = 4 * (XD * wave + j) + (lane >> 4), q = (lane & 15) ^ (r & 15);
-      xoff[j] = (uint32_t)(r * K * 2 + q * 16);
-      xtail[j] = (KB - 1) * kTileCols + 8 * q < K ? xoff[j] : 0x80000000u;
-    }
-  }
+  const TileRows<HV, WH> tr(a, rt.e, t0, lane);
   const DT *const xrows = static_cast<const DT *>(a.x) + (size_t)rt.m0 * K;
-  auto issue_x = [&](int b) {  // slab b by DMA into stage b % 2
-    if constexpr (DMA) {
-      unsigned char *st = smem + b % 2 * STAGE + XD * wave * 1024;
+  unsigned char *const stages = smem + kg * 2 * STAGE;
+
+  // ---- tokens by DMA, 4 rows a load: slab b into stage s
+  constexpr int XD = DMA ? GM / 4 / kGWaves : 1;
+  uint32_t xoff[XD], xtail[XD];
 #pragma unroll
-      for (int j = 0; j < XD; ++j)
-        dma16(xrows, b < KB ? rows * K * 2 : 0, st + j * 1024, b == KB - 1 ? xtail[j] : xoff[j], b * 256);
+  for (int j = 0; j < XD; ++j) {
+    const int r = 4 * (XD * wave + j) + (lane >> 4), q = (lane & 15) ^ (r & 15);
+    xoff[j] = (uint32_t)(r * K * 2 + q * 16);
+    xtail[j] = (KB - 1) * kTileCols + 8 * q < K ? xoff[j] : 0x80000000u;
+  }
+  auto issue_x = [&](int b, int s) {
+    unsigned char *st = stages + s * STAGE + XD * wave * 1024;
+#pragma unroll
+    for (int j = 0; j < XD; ++j)
+      dma16(xrows, b < KB ? rows * K * 2 : 0, st + j * 1024, b == KB - 1 ? xtail[j] : xoff[j], b * 256);
+  };
+  // ---- or through registers: XR chunks of eight elements a thread, 16 a row
+  constexpr int XR = DMA ? 1 : GM * 16 / kGThreads;
+  struct Rows {
+    u32x4_t v[XR][P::kLoads];
+  };
+  auto load_x = [&](Rows &x, int b) {
+#pragma unroll
+    for (int u = 0; u < XR; ++u) {
+      const int c = u * kGThreads + tid, r = min(c / 16, rows - 1);  // (rows past the last are dropped)
+      load8<DT>(xrows, (uint32_t)r * K, b * kTileCols + c % 16 * 8, K, x.v[u]);
     }
   };
-  // through registers: chunk u of a thread is eight elements, 16 chunks a row
-  constexpr int XR = GM * 16 / kGThreads;
-  u32x4_t xr[DMA ? 1 : XR][P::kLoads];
-  auto load_x = [&](int b) {
-    if constexpr (!DMA) {
+  auto store_x = [&](Rows &x, int b, int s) {
+    unsigned char *st = stages + s * STAGE;
 #pragma unroll
-      for (int u = 0; u < XR; ++u) {
-        const int c = u * kGThreads + tid, r = min(c / 16, rows - 1);  // (rows past the last are dropped)
-        load8<DT>(xrows + (size_t)r * K, min(b, KB - 1) * kTileCols + c % 16 * 8, K, xr[u]);
-      }
-    }
-  };
-  auto store_x = [&]() {
-    if constexpr (!DMA) {
+    for (int u = 0; u < XR; ++u) {
+      const int c = u * kGThreads + tid;
+      if ((b + 1) * kTileCols > K) fix8<DT>(b * kTileCols + c % 16 * 8, K, x.v[u]);
+      const P p = P::of(x.v[u]);
 #pragma unroll
-      for (int u = 0; u < XR; ++u) {
-        const int c = u * kGThreads + tid;
-        const P p = P::of(xr[u]);
-#pragma unroll
-        for (int q = 0; q < P::kParts; ++q)
-          *reinterpret_cast<u32x4_t *>(smem + q * PLANE + slab_off(c / 16, c % 16)) = p.p[q];
-      }
+      for (int q = 0; q < P::kParts; ++q)
+        *reinterpret_cast<u32x4_t *>(st + q * PLANE + slab_off(c / 16, c % 16)) = p.p[q];
     }
   };
 
@@ -286,59 +317,91 @@ __global__ __launch_bounds__(kGThreads, 2) void k_fp4_tiled(Fp4GemmArgs a, int n
 #pragma unroll
     for (int t = 0; t < TT; ++t) acc[i][t] = f32x4_t{0, 0, 0, 0};
 
-  // Slab b with its weights in `w`, and what is loaded meanwhile: the weights
-  // of slab b + 1 into `wn`, its tokens.
-  auto step = [&](int b, const Weights &w, Weights &wn) {
+  // The group's i-th slab with its weights in `w`, and what is loaded meanwhile: the
+  // next one's weights into `wn`, its rows (and those of the one after).
+  Rows x;
+  auto step = [&](int i, const Weights<WT> &w, Weights<WT> &wn) {
+    const int b = kg + i * KS, s = i & 1;
     if constexpr (DMA) {
       // this wave's tokens of b landed (the weights behind them may not have),
-      // its reads of slab b - 1 done, for every wave
+      // its reads of the slab before done, for every wave
       __builtin_amdgcn_s_waitcnt(wait_vmcnt(2 * WT) & ~0x0f00);
       __builtin_amdgcn_s_barrier();
       __builtin_amdgcn_sched_barrier(0);
-      issue_x(b + 1);
+      issue_x(b + KS, s ^ 1);
       __builtin_amdgcn_sched_barrier(0);
-      load_w(wn, b + 1);
+      load_weights<ONCE, HV, WH>(wn, tr, KB, b + KS);
       __builtin_amdgcn_sched_barrier(0);
     } else {
-      __syncthreads();  // slab b - 1 is read out
-      store_x();
-      __syncthreads();
-      load_w(wn, b + 1);
-      load_x(b + 1);
+      __syncthreads();  // slab b is stored, the one before read out
+      store_x(x, b + KS, s ^ 1);
+      load_x(x, b + 2 * KS);
+      load_weights<ONCE, HV, WH>(wn, tr, KB, b + KS);
     }
-    const unsigned char *st = smem + (DMA ? b % 2 * STAGE : 0);
-    float s[WT];
+    const unsigned char *st = stages + s * STAGE;
+    float sc[WT];
 #pragma unroll
-    for (int i = 0; i < WT; ++i) s[i] = scale_of_code(w.s[i] >> 8 * (b % 4) & 255u);
+    for (int i = 0; i < WT; ++i) sc[i] = scale_of_code(w.s[i] >> 8 * (b % 4) & 255u);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       u32x4_t wv[WT];
 #pragma unroll
-      for (int i = 0; i < WT; ++i) wv[i] = e2m1x8_to_bf16(w.c[i][c], s[i]);
+      for (int i = 0; i < WT; ++i) wv[i] = e2m1x8_to_bf16(w.c[i][c], sc[i]);
 #pragma unroll
       for (int t = 0; t < TT; ++t)
 #pragma unroll
         for (int q = 0; q < P::kParts; ++q) {
-          const u32x4_t x = *reinterpret_cast<const u32x4_t *>(st + q * PLANE + slab_off(16 * t + l16, 4 * g + c));
+          const u32x4_t v = *reinterpret_cast<const u32x4_t *>(st + q * PLANE + slab_off(16 * t + l16, 4 * g + c));
 #pragma unroll
-          for (int i = 0; i < WT; ++i) Mma<uint16_t>::step(acc[i][t], wv[i], x);
+          for (int i = 0; i < WT; ++i) Mma<uint16_t>::step(acc[i][t], wv[i], v);
         }
     }
   };
 
-  Weights wa, wb;
-  issue_x(0);
-  __builtin_amdgcn_sched_barrier(0);
-  load_w(wa, 0);
-  load_x(0);
-  int b = 0;
-  for (; b + 1 < KB; b += 2) {
-    step(b, wa, wb);
-    step(b + 1, wb, wa);
+  Weights<WT> wa, wb;
+  if constexpr (DMA) {
+    issue_x(kg, 0);
+    __builtin_amdgcn_sched_barrier(0);
+  } else {
+    load_x(x, kg);
   }
-  if (b < KB) step(b, wa, wb);
+  load_weights<ONCE, HV, WH>(wa, tr, KB, kg);
+  if constexpr (!DMA) {
+    store_x(x, kg, 0);
+    load_x(x, kg + KS);
+  }
+  // (every group makes as many steps, one barrier each; slabs past the last are zeros)
+  const int steps = (KB + KS - 1) / KS;
+  int i = 0;
+  for (; i + 1 < steps; i += 2) {
+    step(i, wa, wb);
+    step(i + 1, wb, wa);
+  }
+  if (i < steps) step(i, wa, wb);
   __builtin_amdgcn_s_waitcnt(0x0f70);  // no load of this workgroup outlives it
 
+  if constexpr (KS > 1) {
+    f32x4_t *const sums = reinterpret_cast<f32x4_t *>(smem) + tid;
+    __syncthreads();
+    if (kg > 0) {
+#pragma unroll
+      for (int i = 0; i < WT; ++i)
+#pragma unroll
+        for (int t = 0; t < TT; ++t) sums[((kg - 1) * WT * TT + i * TT + t) * kGThreads] = acc[i][t];
+    }
+    __syncthreads();
+    if (kg > 0) return;
+#pragma unroll
+    for (int i = 0; i < WT; ++i)
+#pragma unroll
+      for (int t = 0; t < TT; ++t)
+#pragma unroll
+        for (int q = 0; q < KS - 1; ++q) {
+          const f32x4_t o = sums[(q * WT * TT + i * TT + t) * kGThreads];
+#pragma unroll
+          for (int v = 0; v < 4; ++v) acc[i][t][v] += o[v];
+        }
+  }
 #pragma unroll
   for (int t = 0; t < TT; ++t) {
     const int m = 16 * t + l16;
@@ -357,66 +420,116 @@ __global__ __launch_bounds__(kGThreads, 2) void k_fp4_tiled(Fp4GemmArgs a, int n
   }
 }
 
-template <int WT, int TT, bool ONCE, bool DMA, bool SILU, typename DT>
+// -------------------------------------------------------------- short rows
+//
+// Rows of less than 16 bytes: a thread a column, its few weights in registers,
+// every gridDim.z-th row of the expert.
+template <bool SILU, typename DT>
+__global__ __launch_bounds__(256) void k_fp4_short(Fp4GemmArgs a) {
+  constexpr int HV = SILU ? 2 : 1, MOST = 16 / (int)sizeof(DT) - 1;
+  int e, lo, hi;
+  if (!find_expert(a, blockIdx.y, e, lo, hi)) return;
+  const int n = blockIdx.x * 256 + threadIdx.x, r = n % kTileRows;
+  if (n >= a.N) return;
+  float w[HV][MOST];
+#pragma unroll
+  for (int h = 0; h < HV; ++h) {
+    const size_t tile = ((size_t)e * HV + h) * a.NT + n / kTileRows;
+    const uint32_t c = *reinterpret_cast<const uint32_t *>(a.w + tile * kTileBytes + 16 * r);
+    const float s = scale_of_code(a.ws[tile * kScaleBytes + 4 * r]);
+    const u32x4_t v = e2m1x8_to_bf16(c, s);
+#pragma unroll
+    for (int k = 0; k < MOST; ++k) w[h][k] = __uint_as_float(k % 2 ? v[k / 2] & 0xffff0000u : v[k / 2] << 16);
+  }
+  for (int m = lo + blockIdx.z; m < hi; m += gridDim.z) {
+    const DT *x = static_cast<const DT *>(a.x) + (size_t)m * a.K;
+    float y[HV];
+#pragma unroll
+    for (int h = 0; h < HV; ++h) y[h] = 0.f;
+#pragma unroll
+    for (int k = 0; k < MOST; ++k) {
+      if (k >= a.K) break;
+#pragma unroll
+      for (int h = 0; h < HV; ++h) y[h] = fmaf(Elem<DT>::to_f32(x[k]), w[h][k], y[h]);
+    }
+    static_cast<DT *>(a.out)[(size_t)m * a.N + n] =
+        Elem<DT>::from_f32(SILU ? silu_mul<sizeof(DT) == 4>(y[0], y[HV - 1]) : y[0]);
+  }
+}
+
+template <int WT, int TT, int KS, bool ONCE, bool DMA, bool SILU, typename DT>
 hipError_t tiled_t(const Fp4GemmArgs &a, hipStream_t st) {
   constexpr int TILES = kGWaves * WT / (SILU ? 2 : 1), GM = 16 * TT;
-  constexpr int LDS = (DMA ? 2 : 1) * GM * 256 * Parts<DT>::kParts;
-  auto kern = k_fp4_tiled<WT, TT, ONCE, DMA, SILU, DT>;
+  constexpr int SLABS = 2 * KS * GM * 256 * Parts<DT>::kParts, SUMS = (KS - 1) * kGThreads * WT * TT * 16;
+  constexpr int LDS = SLABS > SUMS ? SLABS : SUMS;  // (the sums lie where the slabs were)
+  static_assert(LDS <= 160 * 1024, "");
+  auto kern = k_fp4_tiled<WT, TT, KS, ONCE, DMA, SILU, DT>;
   hipError_t err = hipFuncSetAttribute(reinterpret_cast<const void *>(kern),
                                        hipFuncAttributeMaxDynamicSharedMemorySize, LDS);
   if (err != hipSuccess) return err;
   const int ncols = (a.NT + TILES - 1) / TILES;
   const int ne = a.E < a.R ? a.E : a.R;
   const int tiles = (int)(((long long)a.R + (long long)ne * (GM - 1)) / GM);
-  return launch_kernel(kern, dim3(round_up8(tiles * ncols)), dim3(kGThreads), LDS, st, a, ncols);
+  return launch_kernel(kern, dim3(round_up8(tiles * ncols)), dim3(KS * kGThreads), LDS, st, a, ncols);
 }
 
-template <int NT, int TG, bool SILU, typename DT>
+template <int NT, int W, bool ONCE, bool SILU, typename DT>
 hipError_t stream_t(const Fp4GemmArgs &a, hipStream_t st, int groups) {
-  return launch_kernel(k_fp4_stream<NT, TG, SILU, DT>, dim3((a.NT + NT - 1) / NT, a.E < a.R ? a.E : a.R, groups),
-                       dim3(kSThreads), 0, st, a);
+  return launch_kernel(k_fp4_stream<NT, W, ONCE, SILU, DT>,
+                       dim3((a.NT + NT - 1) / NT, a.E < a.R ? a.E : a.R, groups), dim3(W * kWave), 0, st, a);
 }
 
-// Most workgroups a tiled launch can hold: row tiles of GM rows (each expert's
-// last one short) times column tiles.
-long long tiled_wgs(const Fp4GemmArgs &a, bool silu, int WT, int TT) {
-  const long long GM = 16 * TT, tiles = kGWaves * WT / (silu ? 2 : 1);
+// Most workgroups a launch of row groups of GM rows (each expert's last one short) and
+// column groups of `tiles` weight tiles can hold.
+long long workgroups(const Fp4GemmArgs &a, int GM, int tiles) {
   const long long ne = a.E < a.R ? a.E : a.R;
   return (a.R + ne * (GM - 1)) / GM * ((a.NT + tiles - 1) / tiles);
 }
 
 Fp4Choice choose(const Fp4GemmArgs &a, bool silu, bool bf16) {
-  const int mean = a.R / (a.E < a.R ? a.E : a.R);  // rows an expert, if all are hit
-  if (mean <= 16) return {Fp4Kernel::kStream1, 1};
-  if (bf16 && a.K % 8 == 0) {
-    if (mean >= 96 && tiled_wgs(a, silu, 4, 8) >= 512) return {Fp4Kernel::kTile4x8, 1};
-    if (mean > 40) return {Fp4Kernel::kTile4x4, 1};
-    return {Fp4Kernel::kTile2x2Once, 1};
+  const int ne = a.E < a.R ? a.E : a.R, mean = a.R / ne;  // rows an expert, if all are hit
+  const int H = silu ? 1 : 2;
+  if (a.K < (bf16 ? 8 : 4)) return {Fp4Kernel::kShort, mean < 256 ? mean : 256};
+  if (mean <= 4) {
+    const bool many = a.E > 1 && (long long)ne * ((a.NT + 2 * H - 1) / (2 * H)) >= 512;
+    if (many && !bf16) return {Fp4Kernel::kTile4x1, 1};
+    return {many ? Fp4Kernel::kStream4Once : Fp4Kernel::kStream2, a.R < 128 ? 1 : a.R < 256 ? a.R / 64 : 4};
   }
-  if (mean > 40) return {Fp4Kernel::kRegs4x4, 1};
-  return {Fp4Kernel::kRegs2x2, 1};
+  if (workgroups(a, 16, 4) <= 320) return {Fp4Kernel::kSplit1x1, 1};
+  if (workgroups(a, bf16 ? 32 : 16, 4 * H) <= 384) return {Fp4Kernel::kSplit2x2, 1};
+  if (!bf16)
+    return {mean <= 24 || workgroups(a, 32, 8 * H) < 512 ? Fp4Kernel::kTile4x1 : Fp4Kernel::kTile4x2, 1};
+  if (a.K % 8 == 0 && mean >= 48 && workgroups(a, 64, 8 * H) >= 512) return {Fp4Kernel::kTile4x4, 1};
+  return {a.E > 1 && mean <= 40 ? Fp4Kernel::kTile4x2Once : Fp4Kernel::kTile4x2, 1};
 }
 
 template <bool SILU, typename DT>
 hipError_t launch_t(const Fp4GemmArgs &a, Fp4Choice c, hipStream_t st) {
-  constexpr int NT = SILU ? 1 : 2;
+  constexpr int H = SILU ? 1 : 2;
+  constexpr bool BF16 = sizeof(DT) == 2;
   switch (c.kernel) {
-    case Fp4Kernel::kStream1: return stream_t<NT, 1, SILU, DT>(a, st, c.groups);
-    case Fp4Kernel::kStream2: return stream_t<NT, 2, SILU, DT>(a, st, c.groups);
-    case Fp4Kernel::kTile2x2Once:
-      if constexpr (sizeof(DT) == 2) return tiled_t<2, 2, true, true, SILU, DT>(a, st);
+    case Fp4Kernel::kShort:
+      return launch_kernel(k_fp4_short<SILU, DT>, dim3((a.N + 255) / 256, a.E < a.R ? a.E : a.R, c.groups), dim3(256),
+                           0, st, a);
+    case Fp4Kernel::kStream2: return stream_t<H, 8, false, SILU, DT>(a, st, c.groups);
+    case Fp4Kernel::kSplit1x1: return tiled_t<SILU ? 2 : 1, 1, 4, false, false, SILU, DT>(a, st);
+    case Fp4Kernel::kTile4x2: return tiled_t<4, 2, 1, false, false, SILU, DT>(a, st);
+    case Fp4Kernel::kSplit2x2:
+      // (float32: three parts in LDS, so fewer tokens)
+      if constexpr (BF16) return tiled_t<2, 2, 4, false, false, SILU, DT>(a, st);
+      else return tiled_t<4, 1, 4, false, false, SILU, DT>(a, st);
+    case Fp4Kernel::kTile4x1:
+      if constexpr (!BF16) return tiled_t<4, 1, 1, false, false, SILU, DT>(a, st);
       break;
-    case Fp4Kernel::kTile2x4:
-      if constexpr (sizeof(DT) == 2) return tiled_t<2, 4, false, true, SILU, DT>(a, st);
+    case Fp4Kernel::kStream4Once:
+      if constexpr (BF16) return stream_t<2 * H, 4, true, SILU, DT>(a, st, c.groups);
+      break;
+    case Fp4Kernel::kTile4x2Once:
+      if constexpr (BF16) return tiled_t<4, 2, 1, true, false, SILU, DT>(a, st);
       break;
     case Fp4Kernel::kTile4x4:
-      if constexpr (sizeof(DT) == 2) return tiled_t<4, 4, false, true, SILU, DT>(a, st);
+      if constexpr (BF16) return tiled_t<4, 4, 1, false, true, SILU, DT>(a, st);
       break;
-    case Fp4Kernel::kTile4x8:
-      if constexpr (sizeof(DT) == 2) return tiled_t<4, 8, false, true, SILU, DT>(a, st);
-      break;
-    case Fp4Kernel::kRegs2x2: return tiled_t<2, 2, false, false, SILU, DT>(a, st);
-    case Fp4Kernel::kRegs4x4: return tiled_t<4, 4, false, false, SILU, DT>(a, st);
   }
   return hipErrorInvalidValue;
 }
@@ -439,7 +552,7 @@ hipError_t resolve_fp4_gemm(bool silu, bool bf16) {
   a.R = a.N = a.K = a.E = a.NT = a.KB = a.KQ = 1;
   for (int k = 0; k < kFp4Kernels; ++k) {
     const Fp4Kernel kernel = (Fp4Kernel)k;
-    if (!bf16 && fp4_needs_bf16(kernel)) continue;
+    if (bf16 ? kernel == Fp4Kernel::kTile4x1 : kernel >= Fp4Kernel::kStream4Once) continue;
     const hipError_t e = launch(a, silu, bf16, {kernel, 1}, nullptr);
     if (e != hipSuccess) return e;
   }

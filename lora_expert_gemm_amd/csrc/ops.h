@@ -139,13 +139,17 @@ struct Fp4GemmArgs {
   int R, N, K, E;
   int NT, KB, KQ;
 };
-// Which kernel a product takes: streamed, with 1 or 2 groups of 16 rows at a time
-// and `groups` workgroups to share an expert's groups, or tiled, with weight tiles
-// x token tiles of 16 a wave, the tokens straight into LDS (bf16 rows of whole 16
-// bytes) or through registers; Once: the weights go past the caches.
-enum class Fp4Kernel { kStream1, kStream2, kTile2x2Once, kTile2x4, kTile4x4, kTile4x8, kRegs2x2, kRegs4x4 };
-constexpr int kFp4Kernels = 8;
-constexpr bool fp4_needs_bf16(Fp4Kernel k) { return k >= Fp4Kernel::kTile2x2Once && k <= Fp4Kernel::kTile4x8; }
+// Which kernel a product takes.  Short: rows of less than 16 bytes.  Streamed:
+// workgroups of 4 or 2 weight tiles (SILU: half of them gate), `groups` of them to
+// share an expert's groups of 16 rows.  Split and tiled: weight tiles x token tiles of
+// 16 a wave, split with the contraction over four groups of waves (Split2x2 of
+// float32 rows: 4x1); Once: the weights go past the caches.
+enum class Fp4Kernel {
+  kShort, kStream2, kSplit1x1, kSplit2x2, kTile4x2,
+  kTile4x1,                              // float32 rows
+  kStream4Once, kTile4x2Once, kTile4x4,  // bf16 rows (Tile4x4: of whole 16 bytes)
+};
+constexpr int kFp4Kernels = 9;
 struct Fp4Choice {
   Fp4Kernel kernel;
   int groups;
