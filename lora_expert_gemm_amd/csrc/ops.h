@@ -100,9 +100,9 @@ struct BalanceOut {
   float *prob_sum;  // [E]
   float *loss;      // [2]
 };
-// Workgroups whose sums launch_balance keeps in its workspace (1: none there).
+// Most workgroups whose sums launch_balance keeps in its workspace.
 constexpr int kBalanceChunks = 256;
-int balance_chunks(int T, int E);
+size_t balance_workspace(int T, int E);
 hipError_t launch_balance(const RouterArgs &a, bool bf16, const int *ids, const BalanceOut &o, void *ws,
                           hipStream_t st);
 

@@ -126,10 +126,6 @@ moelora_status router_shape(int32_t T, int32_t E, int32_t k, int32_t dtype, Rout
   *a = RouterArgs{nullptr, nullptr, T, E, k};
   return MOELORA_OK;
 }
-size_t balance_ws(const RouterArgs &a) {
-  const int c = balance_chunks(a.T, a.E);
-  return c > 1 ? (size_t)c * (2 * a.E + 2) * 4 : 0;
-}
 
 constexpr long long kMaxTileFours = 1ll << 26;  // (a launch holds fewer than 2^32 threads)
 // Sizes of 4-bit weights; the pointers are left null.
@@ -349,7 +345,7 @@ moelora_status moelora_balance_loss_workspace(int32_t n_tokens, int32_t n_expert
   if (!workspace_bytes) return MOELORA_ERR_INVALID_ARG;
   RouterArgs a;
   const moelora_status st = router_shape(n_tokens, n_experts, top_k, MOELORA_F32, &a);
-  if (st == MOELORA_OK) *workspace_bytes = balance_ws(a);
+  if (st == MOELORA_OK) *workspace_bytes = balance_workspace(a.T, a.E);
   return st;
 }
 
@@ -362,7 +358,7 @@ moelora_status moelora_balance_loss(int32_t n_tokens, int32_t n_experts, int32_t
   if (st != MOELORA_OK) return st;
   if (!ok16(counts) || !ok16(prob_sum) || !ok16(loss)) return MOELORA_ERR_INVALID_ARG;
   if (n_tokens > 0 && (!ok16(logits) || !opt16(token_mask) || !ok16(topk_ids))) return MOELORA_ERR_INVALID_ARG;
-  const size_t need = balance_ws(a);
+  const size_t need = balance_workspace(a.T, a.E);
   if (need > 0 && !ok16(workspace)) return MOELORA_ERR_INVALID_ARG;
   if (workspace_bytes < need) return MOELORA_ERR_WORKSPACE;
   if ((st = ready()) != MOELORA_OK) return st;
