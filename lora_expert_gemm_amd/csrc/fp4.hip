@@ -9,9 +9,9 @@
 // 2^128, the code below it is taken.  A group with an element that is not finite
 // gets the NaN scale and zero codes.
 //
-// A wave makes four tiles of 16 rows along K: the lane of row r and group g
-// reads its 32 weights of each, and writes 16 bytes of codes a tile and one dword
-// of four scales.
+// A wave makes four tiles of 16 rows along K, "a quad".  On the side of the rows its
+// lanes lie along them, 16 bytes each, so that whole lines move; what a group's lanes hold
+// (4 of 8 bf16 elements, 8 of 4 float32 ones) meets in one entry of the tile.
 #include "common.h"
 #include "fp4.h"
 #include "kernels.h"
@@ -24,167 +24,192 @@ namespace {
 constexpr int kThreads = 256, kWaves = kThreads / kWave;
 constexpr uint32_t kInfBits = 0x7f800000u;
 
-// Which four tiles (a "quad") a wave makes, and its lane's place in them.
+// Which quad a wave makes.
 struct Quad {
   uint32_t tile_row, q;  // of all matrices; along K
-  int n, k0, g;        // row in the matrix; column of its group in the first tile
-  bool some;           // the row exists
+  int n0, k0, mat;       // first row in its matrix, first column
 };
-__device__ __forceinline__ Quad quad_of(const Fp4WeightsArgs &a) {
-  const int lane = threadIdx.x % kWave;
-  const uint32_t id = blockIdx.x * kWaves + threadIdx.x / kWave;  // (fewer than 2^26)
-  Quad q;
+__device__ __forceinline__ bool quad_of(const Fp4WeightsArgs &a, Quad &q) {
+  const uint32_t id = __builtin_amdgcn_readfirstlane(blockIdx.x * kWaves + threadIdx.x / kWave);  // (below 2^26)
   q.tile_row = id / a.KQ;
   q.q = id % a.KQ;
-  q.g = lane / kTileRows;
-  q.n = (int)(q.tile_row % a.NT) * kTileRows + lane % kTileRows;
-  q.k0 = (int)q.q * 4 * kTileCols + q.g * kGroup;
-  q.some = q.n < a.N;
-  return q;
+  q.mat = q.tile_row / a.NT;
+  q.n0 = (int)(q.tile_row % a.NT) * kTileRows;
+  q.k0 = (int)q.q * 4 * kTileCols;
+  return id < (uint32_t)a.mats * a.NT * a.KQ;
 }
-__device__ __forceinline__ bool quad_exists(const Fp4WeightsArgs &a) {
-  return blockIdx.x * kWaves + threadIdx.x / kWave < (uint32_t)a.mats * a.NT * a.KQ;
+__device__ __forceinline__ uint8_t *tile_codes(const Fp4WeightsArgs &a, const Quad &q, int b) {
+  return a.codes + ((size_t)q.tile_row * a.KB + q.q * 4 + b) * kTileBytes;
 }
-__device__ __forceinline__ uint4 *tile_codes(uint8_t *codes, const Fp4WeightsArgs &a, const Quad &q, int b) {
-  return reinterpret_cast<uint4 *>(codes + ((size_t)q.tile_row * a.KB + q.q * 4 + b) * kTileBytes) + threadIdx.x % kWave;
-}
-__device__ __forceinline__ uint32_t *quad_scales(uint8_t *scales, const Fp4WeightsArgs &a, const Quad &q) {
-  return reinterpret_cast<uint32_t *>(scales + ((size_t)q.tile_row * a.KQ + q.q) * kScaleBytes) + threadIdx.x % kWave;
+__device__ __forceinline__ uint32_t *quad_scales(const Fp4WeightsArgs &a, const Quad &q) {
+  return reinterpret_cast<uint32_t *>(a.scales + ((size_t)q.tile_row * a.KQ + q.q) * kScaleBytes);
 }
 
-// 32 elements of a row of K from element c on, zeros past K, as float32.
-template <typename DT>
-__device__ __forceinline__ void load32(const DT *row, int c, int K, bool some, float *f) {
-  typedef u32x4_t mem __attribute__((aligned(2)));
-  constexpr int n = sizeof(DT) * 2, per = 16 / sizeof(DT);
-  if (some && c + kGroup <= K) {
-    const mem *p = reinterpret_cast<const mem *>(row + c);
-    u32x4_t v[n];
-#pragma unroll
-    for (int i = 0; i < n; ++i) v[i] = p[i];
-#pragma unroll
-    for (int i = 0; i < n; ++i) {
-      const Chunk<DT> e = chunk_elems<DT>(v[i]);
-#pragma unroll
-      for (int j = 0; j < per; ++j) f[per * i + j] = Elem<DT>::to_f32(e.v[j]);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kGroup; ++i) f[i] = some && c + i < K ? Elem<DT>::to_f32(row[c + i]) : 0.f;
-  }
-}
+// How a wave's lanes lie on a tile's rows: PER elements (16 bytes) each, LANES a
+// row, ROWS rows at a time, STEPS times.
+template <typename DT> struct Lanes {
+  static constexpr int PER = 16 / (int)sizeof(DT), LANES = kTileCols / PER, ROWS = kWave / LANES,
+                       STEPS = kTileRows / ROWS, GROUP = kGroup / PER;  // lanes a group
+  int r, c;  // row of the step, lane of the row
+  __device__ __forceinline__ Lanes() : r(threadIdx.x % kWave / LANES), c(threadIdx.x % LANES) {}
+  __device__ __forceinline__ int row(int s) const { return s * ROWS + r; }
+  // the lane's entry in the tile, and its bytes in there (half a byte an element)
+  __device__ __forceinline__ int entry(int s) const { return c / GROUP * kTileRows + row(s); }
+  __device__ __forceinline__ int byte(int s) const { return entry(s) * 16 + c % GROUP * (PER / 2); }
+};
+template <int BYTES> struct CodeWord;
+template <> struct CodeWord<4> { typedef uint32_t type; };
+template <> struct CodeWord<2> { typedef uint16_t type; };
 
 template <typename DT>
 __global__ __launch_bounds__(kThreads) void k_quant_fp4(Fp4WeightsArgs a) {
-  if (!quad_exists(a)) return;
-  const Quad q = quad_of(a);
-  const DT *row = static_cast<const DT *>(a.src) + ((size_t)(q.tile_row / a.NT) * a.N + q.n) * a.K;
-  uint32_t scales = 0;
+  typedef Lanes<DT> L;
+  typedef typename CodeWord<L::PER / 2>::type word;
+  typedef u32x4_t mem __attribute__((aligned(2)));
+  Quad q;
+  if (!quad_of(a, q)) return;
+  const L ln;
+  const DT *const w = static_cast<const DT *>(a.src) + ((size_t)q.mat * a.N + q.n0) * a.K;
+  const int rows = min(kTileRows, a.N - q.n0);
+  uint32_t scales[L::STEPS];
 #pragma unroll
-  for (int b = 0; b < 4; ++b) {
-    if (q.q * 4 + b >= (uint32_t)a.KB) break;
-    float f[kGroup];
-    load32<DT>(row, q.k0 + b * kTileCols, a.K, q.some, f);
-    uint32_t m = 0;
+  for (int s = 0; s < L::STEPS; ++s) scales[s] = 0;
+  for (int b = 0; b < 4 && q.q * 4 + b < (uint32_t)a.KB; ++b) {
+    const int k = q.k0 + b * kTileCols + ln.c * L::PER;
+    u32x4_t v[L::STEPS];
 #pragma unroll
-    for (int i = 0; i < kGroup; ++i) m = max(m, __float_as_uint(f[i]) & 0x7fffffffu);
-    // amax = (1 + f) 2^q: amax / 6 <= 2^(q - 2) exactly when 1 + f <= 1.5
-    const int e = max(-125, (int)(m >> 23) - 127 - 2 + ((m & 0x7fffffu) > 0x400000u));
-    const bool odd = m >= kInfBits;
-    const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-    uint32_t c[4];
+    for (int s = 0; s < L::STEPS; ++s) {
+      const DT *row = w + (size_t)min(ln.row(s), rows - 1) * a.K;
+      if (k + L::PER <= a.K) {
+        v[s] = __builtin_nontemporal_load(reinterpret_cast<const mem *>(row + k));
+      } else {
+        Chunk<DT> e;
 #pragma unroll
-    for (int d = 0; d < 4; ++d) {
-      uint32_t w = 0;
-#define MOELORA_PAIR(s) \
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, f[8 * d + 2 * s] * inv, f[8 * d + 2 * s + 1] * inv, 1.f, s)
-      MOELORA_PAIR(0);
-      MOELORA_PAIR(1);
-      MOELORA_PAIR(2);
-      MOELORA_PAIR(3);
-#undef MOELORA_PAIR
-      if (e == 126) {  // 4 2^126 is not finite: 3 2^126 then (codes 6, 14 -> 5, 13)
-        const uint32_t six = w >> 1 & w >> 2 & ~w & 0x11111111u;
-        w -= six;
+        for (int i = 0; i < L::PER; ++i) e.v[i] = k + i < a.K ? row[k + i] : DT(0);
+        v[s] = __builtin_bit_cast(u32x4_t, e);
       }
-      c[d] = odd ? 0u : w;
     }
-    *tile_codes(a.codes, a, q, b) = make_uint4(c[0], c[1], c[2], c[3]);
-    scales |= (odd ? 255u : q.some && q.k0 + b * kTileCols < a.K ? (uint32_t)(e + 127) : 0u) << 8 * b;
+    uint8_t *const tile = tile_codes(a, q, b);
+#pragma unroll
+    for (int s = 0; s < L::STEPS; ++s) {
+      const Chunk<DT> e = chunk_elems<DT>(v[s]);
+      const bool some = ln.row(s) < rows;
+      float f[L::PER];
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < L::PER; ++i) {
+        f[i] = some ? Elem<DT>::to_f32(e.v[i]) : 0.f;
+        m = max(m, __float_as_uint(f[i]) & 0x7fffffffu);
+      }
+#pragma unroll
+      for (int d = 1; d < L::GROUP; d <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
+      // amax = (1 + f) 2^x: amax / 6 <= 2^(x - 2) exactly when 1 + f <= 1.5
+      const int x = max(-125, (int)(m >> 23) - 127 - 2 + ((m & 0x7fffffu) > 0x400000u));
+      const bool odd = m >= kInfBits;
+      const float inv = __uint_as_float((uint32_t)(127 - x) << 23);
+      uint32_t c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0, f[0] * inv, f[1] * inv, 1.f, 0);
+      c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f[2] * inv, f[3] * inv, 1.f, 1);
+      if constexpr (L::PER == 8) {
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f[4] * inv, f[5] * inv, 1.f, 2);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f[6] * inv, f[7] * inv, 1.f, 3);
+      }
+      if (x == 126) c -= c >> 1 & c >> 2 & ~c & 0x11111111u;  // 4 2^126 is not finite: codes 6, 14 -> 5, 13
+      if (odd) c = 0;
+      *reinterpret_cast<word *>(tile + ln.byte(s)) = (word)c;
+      scales[s] |= (odd ? 255u : some && k / kGroup * kGroup < a.K ? (uint32_t)(x + 127) : 0u) << 8 * b;
+    }
   }
-  *quad_scales(a.scales, a, q) = scales;
+  if (ln.c % L::GROUP == 0) {
+#pragma unroll
+    for (int s = 0; s < L::STEPS; ++s) quad_scales(a, q)[ln.entry(s)] = scales[s];
+  }
 }
 
-// Row-major codes, two a byte and ceil(K / 2) bytes a row, with ceil(K / 32) scales.
+// Row-major codes, two a byte and ceil(K / 2) bytes a row, with ceil(K / 32) scales:
+// a group of codes is an entry of a tile as it is.
 __global__ __launch_bounds__(kThreads) void k_pack_fp4(Fp4WeightsArgs a) {
-  if (!quad_exists(a)) return;
-  const Quad q = quad_of(a);
-  const int row_bytes = (a.K + 1) / 2, row_groups = (a.K + kGroup - 1) / kGroup;
-  const size_t r = (size_t)(q.tile_row / a.NT) * a.N + q.n;
-  const uint8_t *row = static_cast<const uint8_t *>(a.src) + r * row_bytes;
-  const uint8_t *rs = a.src_scales + r * row_groups;
   typedef u32x4_t mem __attribute__((aligned(1)));
-  uint32_t scales = 0;
+  Quad q;
+  if (!quad_of(a, q)) return;
+  const int lane = threadIdx.x % kWave, rows = min(kTileRows, a.N - q.n0);
+  const int row_bytes = (a.K + 1) / 2, row_groups = (a.K + kGroup - 1) / kGroup;
+  const size_t r0 = (size_t)q.mat * a.N + q.n0;
+  {
+    // a lane's row and group, of each of the four tiles
+    const int r = lane % kTileRows, g0 = q.k0 / kGroup + lane / kTileRows;
+    const uint8_t *rs = a.src_scales + (r0 + min(r, rows - 1)) * row_groups;
+    uint32_t s = 0;
 #pragma unroll
-  for (int b = 0; b < 4; ++b) {
-    if (q.q * 4 + b >= (uint32_t)a.KB) break;
-    const int k = q.k0 + b * kTileCols, at = k / 2;
-    u32x4_t c = {0, 0, 0, 0};
-    if (q.some && k + kGroup <= a.K) {
-      c = *reinterpret_cast<const mem *>(row + at);
-    } else if (q.some && k < a.K) {
+    for (int b = 0; b < 4; ++b)
+      s |= (r < rows && g0 + 4 * b < row_groups ? (uint32_t)rs[min(g0 + 4 * b, row_groups - 1)] : 0u) << 8 * b;
+    quad_scales(a, q)[lane] = s;
+  }
+  // 16 groups of a row side by side, four rows at a time
+  const int b = lane % 16 / 4, k = q.k0 + lane % 16 * kGroup, at = k / 2;
+  u32x4_t c[4];
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const int r = 4 * s + lane / 16;
+    const uint8_t *row = static_cast<const uint8_t *>(a.src) + (r0 + min(r, rows - 1)) * row_bytes;
+    c[s] = u32x4_t{0, 0, 0, 0};
+    if (r < rows && k + kGroup <= a.K) {
+      c[s] = __builtin_nontemporal_load(reinterpret_cast<const mem *>(row + at));
+    } else if (r < rows && k < a.K) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         uint32_t v = k + 2 * i < a.K ? row[at + i] : 0u;
         if (k + 2 * i + 1 >= a.K) v &= 15u;
-        c[i / 4] |= v << 8 * (i % 4);
+        c[s][i / 4] |= v << 8 * (i % 4);
       }
     }
-    if (q.some && k < a.K) scales |= (uint32_t)rs[k / kGroup] << 8 * b;
-    *tile_codes(a.codes, a, q, b) = __builtin_bit_cast(uint4, c);
   }
-  *quad_scales(a.scales, a, q) = scales;
+  if (q.q * 4 + b >= (uint32_t)a.KB) return;
+  uint4 *const tile = reinterpret_cast<uint4 *>(tile_codes(a, q, b));
+#pragma unroll
+  for (int s = 0; s < 4; ++s)
+    tile[lane % 4 * kTileRows + 4 * s + lane / 16] = __builtin_bit_cast(uint4, c[s]);
 }
 
 template <typename DT>
 __global__ __launch_bounds__(kThreads) void k_dequant_fp4(Fp4WeightsArgs a) {
-  if (!quad_exists(a)) return;
-  const Quad q = quad_of(a);
-  const uint32_t scales = *quad_scales(a.scales, a, q);
-  DT *row = static_cast<DT *>(a.dst) + ((size_t)(q.tile_row / a.NT) * a.N + q.n) * a.K;
+  typedef Lanes<DT> L;
+  typedef typename CodeWord<L::PER / 2>::type word;
   typedef u32x4_t mem __attribute__((aligned(2)));
-  constexpr int per = 16 / sizeof(DT);
+  Quad q;
+  if (!quad_of(a, q)) return;
+  const L ln;
+  DT *const w = static_cast<DT *>(a.dst) + ((size_t)q.mat * a.N + q.n0) * a.K;
+  const int rows = min(kTileRows, a.N - q.n0);
+  uint32_t scales[L::STEPS];
 #pragma unroll
-  for (int b = 0; b < 4; ++b) {
-    const int k = q.k0 + b * kTileCols;
-    if (!q.some || k >= a.K) break;
-    const uint4 c = *tile_codes(a.codes, a, q, b);
-    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-    const float s = scale_of_code(scales >> 8 * b & 255u);
-    u32x4_t v[32 / per];
+  for (int s = 0; s < L::STEPS; ++s) scales[s] = quad_scales(a, q)[ln.entry(s)];
+  for (int b = 0; b < 4 && q.q * 4 + b < (uint32_t)a.KB; ++b) {
+    const int k = q.k0 + b * kTileCols + ln.c * L::PER;
+    const uint8_t *const tile = tile_codes(a, q, b);
+    uint32_t c[L::STEPS];
 #pragma unroll
-    for (int d = 0; d < 4; ++d) {
+    for (int s = 0; s < L::STEPS; ++s) c[s] = *reinterpret_cast<const word *>(tile + ln.byte(s));
+#pragma unroll
+    for (int s = 0; s < L::STEPS; ++s) {
+      const float sc = scale_of_code(scales[s] >> 8 * b & 255u);
+      u32x4_t v;
       if constexpr (sizeof(DT) == 2) {
-        v[d] = e2m1x8_to_bf16(w[d], s);
+        v = e2m1x8_to_bf16(c[s], sc);
       } else {
         typedef float f32x2_t __attribute__((ext_vector_type(2)));
-        const f32x2_t p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[d], s, 0),
-                      p1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[d], s, 1),
-                      p2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[d], s, 2),
-                      p3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[d], s, 3);
-        v[2 * d] = __builtin_bit_cast(u32x4_t, f32x4_t{p0[0], p0[1], p1[0], p1[1]});
-        v[2 * d + 1] = __builtin_bit_cast(u32x4_t, f32x4_t{p2[0], p2[1], p3[0], p3[1]});
+        const f32x2_t lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[s], sc, 0),
+                      hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[s], sc, 1);
+        v = __builtin_bit_cast(u32x4_t, f32x4_t{lo[0], lo[1], hi[0], hi[1]});
       }
-    }
-#pragma unroll
-    for (int i = 0; i < 32 / per; ++i) {
-      if (k + (i + 1) * per <= a.K) {
-        *reinterpret_cast<mem *>(row + k + i * per) = v[i];
+      DT *row = w + (size_t)ln.row(s) * a.K;
+      if (ln.row(s) >= rows) continue;
+      if (k + L::PER <= a.K) {
+        __builtin_nontemporal_store(v, reinterpret_cast<mem *>(row + k));
       } else {
-        const Chunk<DT> e = chunk_elems<DT>(v[i]);
+        const Chunk<DT> e = chunk_elems<DT>(v);
 #pragma unroll
-        for (int j = 0; j < per; ++j)
-          if (k + i * per + j < a.K) row[k + i * per + j] = e.v[j];
+        for (int i = 0; i < L::PER; ++i)
+          if (k + i < a.K) row[k + i] = e.v[i];
       }
     }
   }
