@@ -452,7 +452,8 @@ MOELORA_API moelora_status moelora_dequantize_weights_fp4(int32_t n_mats, int32_
  * Entries of expert_start are clamped into [0, M]; they must not fall.
  * With MOELORA_FP4_SILU_MUL the weights of an expert are two matrices, gate
  * then up (mats = 2 E), and out = SiLU(gate) * up, in float32 as of
- * moelora_fp8_gemm.  Limits: those of the weights and M <= 2^24, E <= 1024. */
+ * moelora_fp8_gemm.  Limits: those of the weights and M <= 2^24, M N <= 2^34,
+ * E <= 1024. */
 #define MOELORA_FP4_SILU_MUL 1u
 MOELORA_API moelora_status moelora_fp4_gemm(int32_t n_rows, int32_t n_out, int32_t width,
                                int32_t n_experts, int32_t dtype, uint32_t flags, const void *x,

@@ -338,6 +338,7 @@ __global__ __launch_bounds__(KS * kGThreads, KS > 1 || WT * TT <= 4 ? 4 : WT * T
       load_x(x, b + 2 * KS);
       load_weights<ONCE, HV, WH>(wn, tr, KB, b + KS);
     }
+    if (t0 >= a.NT) return;  // (a wave without columns only helps with the tokens)
     const unsigned char *st = stages + s * STAGE;
     float sc[WT];
 #pragma unroll
@@ -486,6 +487,23 @@ long long workgroups(const Fp4GemmArgs &a, int GM, int tiles) {
   return (a.R + ne * (GM - 1)) / GM * ((a.NT + tiles - 1) / tiles);
 }
 
+// Which kernel, by the mean rows of an expert and by how many workgroups it leaves
+// (256 CUs).  us on one card; "g": by tokens, 32 experts, top-4, 2880 -> 2 x 2880 with
+// SILU, bf16; "d": by rows, one expert, 4096 -> 11008.
+//   few rows, many experts: four weight tiles a workgroup without LDS against tiles whose
+//     tokens go through it: g16 37 / 43 (4x2), g64 57 / 48, g128 96 / 62 (16 tokens of
+//     float32 58 / 49, by 4x1: they stay with tiles)
+//   few rows, few workgroups: two weight tiles and eight waves on the contraction: d1 7.1
+//     (four tiles and waves 8.6, split tiles 7.8)
+//   little work: tiles with the contraction split over four groups of waves.  1x1: d16 8.0
+//     (streamed 9.5 to 12, not split 17), 16 experts x 8 rows 4000 -> 500 8.0 (10.8), d64 16.2;
+//     2x2: d64 13.0 (not split 20), 256 rows 4096 -> 4096 13.4 (17.4), 1000 rows of 8 experts
+//     8000 -> 300 24 (29 by 1x1); float32 4x1: d64 23 (37)
+//   float32: 4x1 against 4x2, 21 rows an expert of 128, 2050 -> 771 48 / 58; 128 rows an
+//     expert of 32 374 / 351
+//   bf16: 4x2 past the caches or through them g64 47 / 54, g256 79 / 78; 4x4 against 4x2
+//     g256 76 / 78, g1024 142 / 167, g6400 684 / 801; of rows that are no whole 16 bytes
+//     (2879 columns) 161 / 167 and 781 / 854, 4000 rows of 64 experts 511 -> 600 27.5 / 25.4
 Fp4Choice choose(const Fp4GemmArgs &a, bool silu, bool bf16) {
   const int ne = a.E < a.R ? a.E : a.R, mean = a.R / ne;  // rows an expert, if all are hit
   const int H = silu ? 1 : 2;
@@ -499,7 +517,8 @@ Fp4Choice choose(const Fp4GemmArgs &a, bool silu, bool bf16) {
   if (workgroups(a, bf16 ? 32 : 16, 4 * H) <= 384) return {Fp4Kernel::kSplit2x2, 1};
   if (!bf16)
     return {mean <= 24 || workgroups(a, 32, 8 * H) < 512 ? Fp4Kernel::kTile4x1 : Fp4Kernel::kTile4x2, 1};
-  if (a.K % 8 == 0 && mean >= 48 && workgroups(a, 64, 8 * H) >= 512) return {Fp4Kernel::kTile4x4, 1};
+  if (mean >= 48 && workgroups(a, 64, 8 * H) >= 512)
+    return {a.K % 8 == 0 ? Fp4Kernel::kTile4x4 : Fp4Kernel::kTile4x4Regs, 1};
   return {a.E > 1 && mean <= 40 ? Fp4Kernel::kTile4x2Once : Fp4Kernel::kTile4x2, 1};
 }
 
@@ -529,6 +548,9 @@ hipError_t launch_t(const Fp4GemmArgs &a, Fp4Choice c, hipStream_t st) {
       break;
     case Fp4Kernel::kTile4x4:
       if constexpr (BF16) return tiled_t<4, 4, 1, false, true, SILU, DT>(a, st);
+      break;
+    case Fp4Kernel::kTile4x4Regs:
+      if constexpr (BF16) return tiled_t<4, 4, 1, false, false, SILU, DT>(a, st);
       break;
   }
   return hipErrorInvalidValue;

@@ -141,6 +141,7 @@ moelora_status fp4_shape(int32_t mats, int32_t N, int32_t K, Fp4WeightsArgs *a) 
   return (long long)mats * a->NT * a->KQ < kMaxTileFours ? MOELORA_OK : MOELORA_ERR_UNSUPPORTED;
 }
 
+constexpr long long kMaxResults = 1ll << 34;  // (a thread of a tile makes eight and more)
 // Sizes of the product on 4-bit weights; the pointers are left null.
 moelora_status fp4_gemm_shape(int32_t n_rows, int32_t n_out, int32_t width, int32_t n_experts, int32_t dtype,
                               uint32_t flags, Fp4GemmArgs *a) {
@@ -149,6 +150,7 @@ moelora_status fp4_gemm_shape(int32_t n_rows, int32_t n_out, int32_t width, int3
       (dtype != MOELORA_F32 && dtype != MOELORA_BF16))
     return MOELORA_ERR_UNSUPPORTED;
   Fp4WeightsArgs w{};
+  if ((long long)n_rows * n_out > kMaxResults) return MOELORA_ERR_UNSUPPORTED;
   const moelora_status st = fp4_shape(n_experts * (flags & MOELORA_FP4_SILU_MUL ? 2 : 1), n_out, width, &w);
   *a = Fp4GemmArgs{};
   a->R = n_rows;
@@ -465,8 +467,8 @@ moelora_status moelora_fp4_gemm_info(int32_t n_rows, int32_t n_out, int32_t widt
     snprintf(buf, buf_len, "kernel=none");
     return MOELORA_OK;
   }
-  static const char *const names[kFp4Kernels] = {"short",   "stream2", "split1x1",     "split2x2",    "tile4x2",
-                                                 "tile4x1", "stream4_once", "tile4x2_once", "tile4x4"};
+  static const char *const names[kFp4Kernels] = {"short",   "stream2",      "split1x1",     "split2x2", "tile4x2",
+                                                 "tile4x1", "stream4_once", "tile4x2_once", "tile4x4",  "tile4x4_regs"};
   const Fp4Choice c = choose_fp4_gemm(a, flags & MOELORA_FP4_SILU_MUL, dtype == MOELORA_BF16);
   snprintf(buf, buf_len, "kernel=%s groups=%d", names[(int)c.kernel], c.groups);
   return MOELORA_OK;

@@ -142,6 +142,7 @@ def gemm(M=4, N=8, K=8, E=1, dtype=lib.F32, flags=0, x=A, start=None, w=A, ws=A,
 @pytest.mark.parametrize("bad,want", [
     (dict(M=-1), BAD),
     (dict(M=(1 << 24) + 1), NOT),
+    (dict(M=(1 << 24) - 1, N=1026), NOT),            # more results than a launch makes
     (dict(N=0), NOT),
     (dict(N=131073), NOT),
     (dict(K=0), NOT),
