@@ -368,7 +368,9 @@ __global__ __launch_bounds__(kSumThreads) void k_balance(RouterArgs a, const int
 // Second launch: EX experts a workgroup, its threads spread over the chunks, added
 // in 64 bits and in a fixed order.  Where there are several workgroups, the one that
 // is last to finish adds up their shares of the loss (in the same order whichever
-// it is).  16 experts a workgroup, or all of up to 128.
+// it is).  16 experts a workgroup, or all of up to 128 where the chunks are few: one
+// workgroup reads some 40 GB/s (6400 tokens of 32 experts 7.4 us, by several 8.4; 65521 of
+// 128 16.5, by several 14.6).
 constexpr int kFinishFew = 16, kFinishAll = 128;
 template <int EX>
 __global__ __launch_bounds__(kSumThreads) void k_balance_finish(RouterArgs a, BalanceOut o, ChunkSums c) {
@@ -643,7 +645,7 @@ template <typename DT> struct BalanceLaunch {
     c.loss = reinterpret_cast<double *>(c.done + 2);
     hipError_t e = launch_kernel(k_balance<L, S, DT>, dim3(chunks), dim3(kSumThreads), 0, st, a, ids, o, c);
     if (e != hipSuccess || (chunks == 1 && !tl_resolve_only)) return e;
-    if (a.E <= kFinishAll || tl_resolve_only) {
+    if ((a.E <= kFinishAll && chunks * a.E <= 4096) || tl_resolve_only) {
       e = launch_kernel(k_balance_finish<kFinishAll>, dim3(1), dim3(kSumThreads), 0, st, a, o, c);
       if (e != hipSuccess || !tl_resolve_only) return e;
     }
