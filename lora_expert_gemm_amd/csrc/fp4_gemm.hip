@@ -243,6 +243,39 @@ constexpr int kGWaves = 4, kGThreads = kGWaves * kWave;
 // at one chunk fall on 16 distinct bank groups.
 __device__ __forceinline__ int slab_off(int row, int q) { return row * 256 + ((q ^ (row & 15)) << 4); }
 
+// Results of a token, WH neighbouring weight tiles from column n0 on, lane g holding
+// columns 4 g .. + 3 of each: two tiles' lanes g and g + 1 change places, so that a lane
+// has eight columns of one tile and stores 16 bytes, 64 of a row side by side (8 and 32
+// without: 10750 rows of 23 experts 71 -> 1268 14.9 -> 14.0 us, 4096 of 32 gate_up 144 -> 140).
+template <int WH>
+__device__ __forceinline__ void store_pairs(uint16_t *row, bool some, int n0, int g, int N, const float (*o)[4]) {
+  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+  typedef u32x4_t mem __attribute__((aligned(2)));
+#pragma unroll
+  for (int i = 0; i < WH; i += 2) {
+    uint32_t a[2], b[2];
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      a[v] = __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)o[i][2 * v], (__bf16)o[i][2 * v + 1]});
+      b[v] = __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)o[i + 1][2 * v], (__bf16)o[i + 1][2 * v + 1]});
+      // rows of 16 lanes: a's odd ones change places with b's even ones
+      const auto s = __builtin_amdgcn_permlane16_swap(a[v], b[v], false, false);
+      a[v] = s[0], b[v] = s[1];
+    }
+    const int n = n0 + (i + (g & 1)) * kTileRows + 8 * (g >> 1);
+    const u32x4_t w = {a[0], a[1], b[0], b[1]};
+    if (!some) continue;
+    if (n + 8 <= N) {
+      *reinterpret_cast<mem *>(row + n) = w;
+    } else {
+      const Chunk<uint16_t> e = chunk_elems<uint16_t>(w);
+#pragma unroll
+      for (int v = 0; v < 8; ++v)
+        if (n + v < N) row[n + v] = e.v[v];
+    }
+  }
+}
+
 // 16 bytes a lane from `base` + voff + soff into 1 KB of LDS; zeros where they lie
 // past `bytes`.
 __device__ __forceinline__ void dma16(const void *base, int bytes, unsigned char *lds, uint32_t voff, int soff) {
@@ -406,17 +439,21 @@ __global__ __launch_bounds__(KS * kGThreads, KS > 1 || WT * TT <= 4 ? 4 : WT * T
 #pragma unroll
   for (int t = 0; t < TT; ++t) {
     const int m = 16 * t + l16;
-    if (m >= rows) continue;
-    DT *row = static_cast<DT *>(a.out) + (size_t)(rt.m0 + m) * a.N;
+    DT *row = static_cast<DT *>(a.out) + (size_t)(rt.m0 + min(m, rows - 1)) * a.N;
+    float o[WH][4];
 #pragma unroll
-    for (int i = 0; i < WH; ++i) {
-      const int n = (t0 + i) * kTileRows + 4 * g;
-      if (n >= a.N) continue;
-      float o[4];
+    for (int i = 0; i < WH; ++i)
 #pragma unroll
       for (int v = 0; v < 4; ++v)
-        o[v] = SILU ? silu_mul<sizeof(DT) == 4>(acc[i][t][v], acc[(i + WH) % WT][t][v]) : acc[i][t][v];
-      store4<DT>(row, n, a.N, o);
+        o[i][v] = SILU ? silu_mul<sizeof(DT) == 4>(acc[i][t][v], acc[(i + WH) % WT][t][v]) : acc[i][t][v];
+    if constexpr (sizeof(DT) == 2 && WH % 2 == 0) {
+      store_pairs<WH>(row, m < rows, t0 * kTileRows, g, a.N, o);
+    } else {
+#pragma unroll
+      for (int i = 0; i < WH; ++i) {
+        const int n = (t0 + i) * kTileRows + 4 * g;
+        if (m < rows && n < a.N) store4<DT>(row, n, a.N, o[i]);
+      }
     }
   }
 }
@@ -498,9 +535,14 @@ long long workgroups(const Fp4GemmArgs &a, int GM, int tiles) {
 //   little work: tiles with the contraction split over four groups of waves.  1x1: d16 8.0
 //     (streamed 9.5 to 12, not split 17), 16 experts x 8 rows 4000 -> 500 8.0 (10.8), d64 16.2;
 //     2x2: d64 13.0 (not split 20), 256 rows 4096 -> 4096 13.4 (17.4), 1000 rows of 8 experts
-//     8000 -> 300 24 (29 by 1x1); float32 4x1: d64 23 (37)
+//     8000 -> 300 24 (29 by 1x1); float32 4x1: d64 23 (37).  Its sixteen
+//     waves fill a CU: with more workgroups than CUs 2300 rows of 5 experts 1024 -> 446 12.5
+//     (9.0), 3735 float32 rows of 94 948 -> 98 19.7 (14.1; with four column groups and more
+//     the rows come from caches, 1024 rows of 8 2048 -> 625 14.6 (17.1))
 //   float32: 4x1 against 4x2, 21 rows an expert of 128, 2050 -> 771 48 / 58; 128 rows an
 //     expert of 32 374 / 351
+//   bf16, a few workgroups a CU, rows straight into LDS: 2x2 against 4x2: 1024 rows of 8
+//     2048 -> 1250 11.4 / 13.7, -> 2600 17.1 / 19.9, -> 6000 34.5 / 30.9 (4x4)
 //   bf16: 4x2 past the caches or through them g64 47 / 54, g256 79 / 78; 4x4 against 4x2
 //     g256 76 / 78, g1024 142 / 167, g6400 684 / 801; of rows that are no whole 16 bytes
 //     (2879 columns) 161 / 167 and 781 / 854, 4000 rows of 64 experts 511 -> 600 27.5 / 25.4
@@ -514,9 +556,11 @@ Fp4Choice choose(const Fp4GemmArgs &a, bool silu, bool bf16) {
     return {many ? Fp4Kernel::kStream4Once : Fp4Kernel::kStream2, a.R < 128 ? 1 : a.R < 256 ? a.R / 64 : 4};
   }
   if (workgroups(a, 16, 4) <= 320) return {Fp4Kernel::kSplit1x1, 1};
-  if (workgroups(a, bf16 ? 32 : 16, 4 * H) <= 384) return {Fp4Kernel::kSplit2x2, 1};
+  const long long split = workgroups(a, bf16 ? 32 : 16, 4 * H);
+  if (split <= (bf16 || a.NT <= 12 * H ? 288 : 384)) return {Fp4Kernel::kSplit2x2, 1};
   if (!bf16)
     return {mean <= 24 || workgroups(a, 32, 8 * H) < 512 ? Fp4Kernel::kTile4x1 : Fp4Kernel::kTile4x2, 1};
+  if (a.K % 8 == 0 && (mean > 40 || a.E == 1) && split <= 1024) return {Fp4Kernel::kTile2x2, 1};
   if (mean >= 48 && workgroups(a, 64, 8 * H) >= 512)
     return {a.K % 8 == 0 ? Fp4Kernel::kTile4x4 : Fp4Kernel::kTile4x4Regs, 1};
   return {a.E > 1 && mean <= 40 ? Fp4Kernel::kTile4x2Once : Fp4Kernel::kTile4x2, 1};
@@ -542,6 +586,9 @@ hipError_t launch_t(const Fp4GemmArgs &a, Fp4Choice c, hipStream_t st) {
       break;
     case Fp4Kernel::kStream4Once:
       if constexpr (BF16) return stream_t<2 * H, 4, true, SILU, DT>(a, st, c.groups);
+      break;
+    case Fp4Kernel::kTile2x2:
+      if constexpr (BF16) return tiled_t<2, 2, 1, false, true, SILU, DT>(a, st);
       break;
     case Fp4Kernel::kTile4x2Once:
       if constexpr (BF16) return tiled_t<4, 2, 1, true, false, SILU, DT>(a, st);

@@ -147,9 +147,9 @@ struct Fp4GemmArgs {
 enum class Fp4Kernel {
   kShort, kStream2, kSplit1x1, kSplit2x2, kTile4x2,
   kTile4x1,                              // float32 rows
-  kStream4Once, kTile4x2Once, kTile4x4, kTile4x4Regs,  // bf16 rows (Tile4x4: of whole 16 bytes, straight into LDS)
+  kStream4Once, kTile2x2, kTile4x2Once, kTile4x4, kTile4x4Regs,  // bf16 rows (2x2, 4x4: whole 16 bytes, by DMA)
 };
-constexpr int kFp4Kernels = 10;
+constexpr int kFp4Kernels = 11;
 struct Fp4Choice {
   Fp4Kernel kernel;
   int groups;

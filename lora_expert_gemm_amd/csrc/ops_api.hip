@@ -467,8 +467,9 @@ moelora_status moelora_fp4_gemm_info(int32_t n_rows, int32_t n_out, int32_t widt
     snprintf(buf, buf_len, "kernel=none");
     return MOELORA_OK;
   }
-  static const char *const names[kFp4Kernels] = {"short",   "stream2",      "split1x1",     "split2x2", "tile4x2",
-                                                 "tile4x1", "stream4_once", "tile4x2_once", "tile4x4",  "tile4x4_regs"};
+  static const char *const names[kFp4Kernels] = {"short",   "stream2",      "split1x1", "split2x2",     "tile4x2",
+                                                 "tile4x1", "stream4_once", "tile2x2",  "tile4x2_once", "tile4x4",
+                                                 "tile4x4_regs"};
   const Fp4Choice c = choose_fp4_gemm(a, flags & MOELORA_FP4_SILU_MUL, dtype == MOELORA_BF16);
   snprintf(buf, buf_len, "kernel=%s groups=%d", names[(int)c.kernel], c.groups);
   return MOELORA_OK;

@@ -52,8 +52,10 @@ CASES = [
     ("tile4x1", (F,), 0, "many_few", 520, (1003,)),
     ("tile4x2", (F,), 0, "hundreds", 4100, (384, 1003)),
     ("tile4x2", (F,), 1, "hundreds", 2050, (384, 1003)),
-    ("tile4x2", (B,), 0, "hundreds", 1500, (384, 1003)),
-    ("tile4x2", (B,), 1, "eighty", 1500, (384, 1003)),
+    ("tile4x2", (B,), 0, "hundreds", 1500, (385, 1003)),
+    ("tile4x2", (B,), 1, "eighty", 1500, (385, 1003)),
+    ("tile2x2", (B,), 0, "hundreds", 1500, (384, 1000, 2600)),
+    ("tile2x2", (B,), 1, "eighty", 1500, (384, 1000, 2600)),
     ("tile4x2_once", (B,), 0, "mid", 8100, (384, 1003)),
     ("tile4x2_once", (B,), 1, "mid", 4100, (384, 1003, 2600)),
     ("tile4x4", (B,), 0, "hundreds", 9001, (384, 1000)),
@@ -73,7 +75,7 @@ def test_each_case_takes_its_kernel():
     for name, dtype, silu, rows, N, K in FLAT:
         assert kernel(rows, N, K, dtype, silu) == name, (rows, N, K, dtype, silu)
     common = {"short", "stream2", "split1x1", "split2x2", "tile4x2"}
-    for dtype, own in ((F, {"tile4x1"}), (B, {"stream4_once", "tile4x2_once", "tile4x4", "tile4x4_regs"})):
+    for dtype, own in ((F, {"tile4x1"}), (B, {"stream4_once", "tile2x2", "tile4x2_once", "tile4x4", "tile4x4_regs"})):
         for silu in (0, 1):
             assert {c[0] for c in FLAT if c[1] == dtype and c[2] == silu} == common | own
 
