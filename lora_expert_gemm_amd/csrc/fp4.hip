@@ -12,6 +12,9 @@
 // A wave makes four tiles of 16 rows along K, "a quad".  On the side of the rows its
 // lanes lie along them, 16 bytes each, so that whole lines move; what a group's lanes hold
 // (4 of 8 bf16 elements, 8 of 4 float32 ones) meets in one entry of the tile.
+//
+// Bound by HBM: 16 x 11008 x 4096 bf16 made into codes in 300 us (6.1 TB/s, mostly read)
+// and back in 375 (4.9 TB/s, mostly written; a large copy 5.0).
 #include "common.h"
 #include "fp4.h"
 #include "kernels.h"

@@ -143,7 +143,9 @@ __device__ __forceinline__ void load_weights(Weights<HV * WH> &w, const TileRows
 // up to 16 of its tokens at a time (every gridDim.z-th group); its W waves take every
 // W-th tile along the contraction, one ahead, and add their sums through LDS in
 // wave order, so that a narrow product still fills the chip.  Weights go from
-// memory straight into registers, 1 KB a load, tokens too.
+// memory straight into registers, 1 KB a load, tokens too.  Bound by the weights' bytes:
+// 64 rows on 23 of 32 experts, 2880 -> 2 x 2880 38 us, 5.75 TB/s; one row, 4096 -> 11008, 7.6,
+// one round of 344 workgroups whose start and end weigh as much as their loads.
 template <int NT, int W, bool ONCE, bool SILU, typename DT>
 __global__ __launch_bounds__(W * kWave) void k_fp4_stream(Fp4GemmArgs a) {
   constexpr int HV = SILU ? 2 : 1, A = HV * NT, XL = Parts<DT>::kLoads;
@@ -237,10 +239,16 @@ __global__ __launch_bounds__(W * kWave) void k_fp4_stream(Fp4GemmArgs a) {
 // end, so their loads fetch nothing and give zeros.  Otherwise (float32 rows, in
 // their three parts; bf16 rows of any length) they pass through registers, a slab
 // ahead of their stage.
+//
+// Many rows are bound by the matrix cores: 25600 rows of 32 experts, 2880 -> 2 x 2880 with
+// SILU 680 us, 1.25 PFLOP/s (8192^3 1.39, as the library's bf16 product), the cores busy 70 %
+// of the cycles.  With some 20 rows an expert (2664 float32 rows of 128, 2050 -> 771, 48 us) a
+// slab's latency and the weights' conversion weigh as much as the products: cores busy 32 %.
 constexpr int kGWaves = 4, kGThreads = kGWaves * kWave;
 
 // LDS byte offset of 16-byte chunk q of a 256-byte row: 16 consecutive rows read
-// at one chunk fall on 16 distinct bank groups.
+// at one chunk fall on 16 distinct bank groups.  (Lanes of two chunks are served together
+// and may meet, 3.8 cycles a read; an order in which none do was no faster.)
 __device__ __forceinline__ int slab_off(int row, int q) { return row * 256 + ((q ^ (row & 15)) << 4); }
 
 // Results of a token, WH neighbouring weight tiles from column n0 on, lane g holding
