@@ -187,7 +187,7 @@ def check_balance(t, ids, mask, got):
 
 @pytest.mark.parametrize("dtype", [lib.F32, lib.BF16])
 @pytest.mark.parametrize("T,E,k", SIZES + [(3000, 40, 4), (4099, 128, 8), (9000, 300, 3), (40_000, 6, 2),
-                                           (3001, 1024, 2)])
+                                           (3001, 1024, 2), (20_000, 37, 4)])
 def test_balance(T, E, k, dtype):
     say(f"[router] balance T={T} E={E} k={k} {DT[dtype]}")
     for off, masked in ((0, False), (min(2, E - 1), True), (E, False)):
