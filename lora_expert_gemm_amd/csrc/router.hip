@@ -532,7 +532,8 @@ __global__ __launch_bounds__(kThreads) void k_route_backward(RouterArgs a, Route
         cp = fmaf(c[i], r.v[i], cp);
       }
       cp = group_sum<L>(cp);
-      const float rest = cz * (top + logf(sum)) - (ALL ? dot : 0.f);
+      // (of infinite logits lse is infinite: nothing of it where its loss has no gradient)
+      const float rest = (cz != 0.f ? cz * (top + logf(sum)) : 0.f) - (ALL ? dot : 0.f);
 #pragma unroll
       for (int i = 0; i < S; ++i) d[i] = r.v[i] > 0.f ? r.v[i] * fmaf(ca, c[i] - cp, rest) : 0.f;
     } else {

@@ -333,6 +333,24 @@ def test_backward_of_repeated_and_bad_ids():
         check_backward(got, ref, tol)
 
 
+@pytest.mark.parametrize("flags", [0, ALL])
+@pytest.mark.parametrize("dtype", [lib.F32, lib.BF16])
+def test_backward_of_infinite_logits(dtype, flags):
+    """Two logits of +inf share a token: p = 1/2 each, 0 elsewhere, and the logarithm of the
+    sum, which is infinite, adds nothing where its loss has no gradient.  Every number here is
+    a float of few bits, so the sums are exact."""
+    inf, nan = float("inf"), float("nan")
+    t = torch.tensor([[inf, 1, 2, inf, nan], [nan] * 5]).to(DT[dtype])
+    ids, w = run_route(t, 4, dtype, flags)
+    assert ids.tolist() == [[0, 3, 2, 1], [-1] * 4] and w.tolist() == [[.5, .5, 0, 0], [0] * 4]
+    dw = cu(np.array([[1, 3, 5, 7], [nan] * 4], np.float32))
+    counts, dloss = cu(np.array([3, 0, 0, 1, 0, 1], np.int32)), cu(np.array([1, 0], np.float32))
+    by_w, by_loss = np.array([-.5, 0, 0, .5, 0]), np.array([.625, 0, 0, -.625, 0])
+    for a, b in ((1, 0), (0, 1), (1, 1)):
+        d = run_backward(t, 4, dtype, flags, ids, w, dw if a else None, counts if b else None, dloss if b else None)
+        assert d.tolist() == [list(a * by_w + b * by_loss), [0] * 5]
+
+
 def test_gradient_of_a_nearly_balanced_batch():
     """Counts of 2^20 and a few: taking off their mean leaves the few exactly, where
     c_i - sum c p in float32 would be off by 2^20 u = 0.06 of one."""
