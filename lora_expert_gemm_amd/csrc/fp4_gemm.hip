@@ -15,6 +15,8 @@
 // to match.  float32 rows are cut into three bf16 parts (the upper, middle and
 // lower eight bits of the significand: their sum is the value itself), and
 // every part meets the weights in turn; sums are float32 throughout.
+#include <algorithm>
+
 #include "common.h"
 #include "fp4.h"
 #include "grouped.h"
@@ -557,7 +559,11 @@ long long workgroups(const Fp4GemmArgs &a, int GM, int tiles) {
 Fp4Choice choose(const Fp4GemmArgs &a, bool silu, bool bf16) {
   const int ne = a.E < a.R ? a.E : a.R, mean = a.R / ne;  // rows an expert, if all are hit
   const int H = silu ? 1 : 2;
-  if (a.K < (bf16 ? 8 : 4)) return {Fp4Kernel::kShort, mean < 256 ? mean : 256};
+  if (a.K < (bf16 ? 8 : 4)) {
+    // (a thread for every 256th row at least, while that leaves at most 2^30 threads)
+    const int most = (1 << 22) / ((a.N + 255) / 256 * ne);
+    return {Fp4Kernel::kShort, std::min({mean, 256, most})};
+  }
   if (mean <= 4) {
     const bool many = a.E > 1 && (long long)ne * ((a.NT + 2 * H - 1) / (2 * H)) >= 512;
     if (many && !bf16) return {Fp4Kernel::kTile4x1, 1};

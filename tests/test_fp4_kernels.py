@@ -80,6 +80,15 @@ def test_each_case_takes_its_kernel():
             assert {c[0] for c in FLAT if c[1] == dtype and c[2] == silu} == common | own
 
 
+def test_workgroups_of_short_rows_are_bounded():
+    """Workgroups of 256 threads for 256 columns, an expert and every so many rows: no more than 2^30
+    threads at the limits, no third dimension past its own."""
+    for R, N, E in ((1 << 17, 131072, 1024), (1 << 24, 1024, 1), (1 << 24, 1, 1024), (1, 1, 1), (5, 131072, 1024)):
+        line = dict(p.split("=") for p in lib.moelora_fp4_gemm_info(R, N, 3, E, B).split())
+        groups, columns = int(line["groups"]), (N + 255) // 256
+        assert line["kernel"] == "short" and 1 <= groups <= 256 and groups * columns * min(E, R) * 256 <= 1 << 30
+
+
 def test_info_refuses():
     assert lib.moelora_fp4_gemm_info(0, 8, 8, 1, F) == "kernel=none"
     for bad in ((-1, 8, 8, 1, F), (4, 0, 8, 1, F), (4, 8, 8, 1025, F), (4, 8, 8, 1, 2), (4, 8, 8, 1, F, 2)):
