@@ -13,8 +13,8 @@
 // lanes lie along them, 16 bytes each, so that whole lines move; what a group's lanes hold
 // (4 of 8 bf16 elements, 8 of 4 float32 ones) meets in one entry of the tile.
 //
-// Bound by HBM: 16 x 11008 x 4096 bf16 made into codes in 300 us (6.1 TB/s, mostly read)
-// and back in 375 (4.9 TB/s, mostly written; a large copy 5.0).
+// Bound by HBM: 16 x 11008 x 4096 bf16 made into codes in 302 us (6.0 TB/s, mostly read)
+// and back in 357 (5.1 TB/s, mostly written; a large copy 5.0).
 #include "common.h"
 #include "fp4.h"
 #include "kernels.h"
@@ -60,11 +60,15 @@ template <typename DT> struct Lanes {
   __device__ __forceinline__ int entry(int s) const { return c / GROUP * kTileRows + row(s); }
   __device__ __forceinline__ int byte(int s) const { return entry(s) * 16 + c % GROUP * (PER / 2); }
 };
+// WHOLE: rows of whole lines pass by the caches; of others, a line's two owners meet there (16 x
+// 11008 x 4090 bf16 quantised 358 us, past the caches 476; 4096 columns, quantised and back in turn,
+// past the caches 656, through them 690).
+template <typename DT> bool whole_lines(int K) { return K % (128 / (int)sizeof(DT)) == 0; }
 template <int BYTES> struct CodeWord;
 template <> struct CodeWord<4> { typedef uint32_t type; };
 template <> struct CodeWord<2> { typedef uint16_t type; };
 
-template <typename DT>
+template <bool WHOLE, typename DT>
 __global__ __launch_bounds__(kThreads) void k_quant_fp4(Fp4WeightsArgs a) {
   typedef Lanes<DT> L;
   typedef typename CodeWord<L::PER / 2>::type word;
@@ -77,14 +81,17 @@ __global__ __launch_bounds__(kThreads) void k_quant_fp4(Fp4WeightsArgs a) {
   uint32_t scales[L::STEPS];
 #pragma unroll
   for (int s = 0; s < L::STEPS; ++s) scales[s] = 0;
-  for (int b = 0; b < 4 && q.q * 4 + b < (uint32_t)a.KB; ++b) {
+  const int tiles = min(4, a.KB - (int)q.q * 4);
+  for (int b = 0; b < tiles; ++b) {
     const int k = q.k0 + b * kTileCols + ln.c * L::PER;
     u32x4_t v[L::STEPS];
 #pragma unroll
     for (int s = 0; s < L::STEPS; ++s) {
       const DT *row = w + (size_t)min(ln.row(s), rows - 1) * a.K;
       if (k + L::PER <= a.K) {
-        v[s] = __builtin_nontemporal_load(reinterpret_cast<const mem *>(row + k));
+        const mem *p = reinterpret_cast<const mem *>(row + k);
+        if constexpr (WHOLE) v[s] = __builtin_nontemporal_load(p);
+        else v[s] = *p;
       } else {
         Chunk<DT> e;
 #pragma unroll
@@ -156,7 +163,7 @@ __global__ __launch_bounds__(kThreads) void k_pack_fp4(Fp4WeightsArgs a) {
     const uint8_t *row = static_cast<const uint8_t *>(a.src) + (r0 + min(r, rows - 1)) * row_bytes;
     c[s] = u32x4_t{0, 0, 0, 0};
     if (r < rows && k + kGroup <= a.K) {
-      c[s] = __builtin_nontemporal_load(reinterpret_cast<const mem *>(row + at));
+      c[s] = *reinterpret_cast<const mem *>(row + at);
     } else if (r < rows && k < a.K) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
@@ -173,49 +180,65 @@ __global__ __launch_bounds__(kThreads) void k_pack_fp4(Fp4WeightsArgs a) {
     tile[lane % 4 * kTileRows + 4 * s + lane / 16] = __builtin_bit_cast(uint4, c[s]);
 }
 
-template <typename DT>
-__global__ __launch_bounds__(kThreads) void k_dequant_fp4(Fp4WeightsArgs a) {
-  typedef Lanes<DT> L;
-  typedef typename CodeWord<L::PER / 2>::type word;
+// A quad's values, the lanes on ROWS rows at a time.
+template <int ROWS, bool WHOLE, typename DT>
+__device__ __forceinline__ void dequant_quad(const Fp4WeightsArgs &a, const Quad &q, uint32_t scales, int width) {
+  constexpr int PER = 16 / (int)sizeof(DT), LANES = kWave / ROWS;
+  typedef typename CodeWord<PER / 2>::type word;
   typedef u32x4_t mem __attribute__((aligned(2)));
-  Quad q;
-  if (!quad_of(a, q)) return;
-  const L ln;
+  const int lane = threadIdx.x % kWave, rows = min(kTileRows, a.N - q.n0), r0 = lane / LANES;
   DT *const w = static_cast<DT *>(a.dst) + ((size_t)q.mat * a.N + q.n0) * a.K;
-  const int rows = min(kTileRows, a.N - q.n0);
-  uint32_t scales[L::STEPS];
+  for (int l0 = 0; l0 < width; l0 += LANES) {
+    const int col = (l0 + lane % LANES) * PER, k = q.k0 + col;
+    const int b = min(col / kTileCols, a.KB - 1 - (int)q.q * 4), g = col % kTileCols / kGroup;
+    const uint8_t *const codes = tile_codes(a, q, b) + (g * kTileRows + r0) * 16 + col % kGroup / 2;
+    uint32_t c[kTileRows / ROWS];
 #pragma unroll
-  for (int s = 0; s < L::STEPS; ++s) scales[s] = quad_scales(a, q)[ln.entry(s)];
-  for (int b = 0; b < 4 && q.q * 4 + b < (uint32_t)a.KB; ++b) {
-    const int k = q.k0 + b * kTileCols + ln.c * L::PER;
-    const uint8_t *const tile = tile_codes(a, q, b);
-    uint32_t c[L::STEPS];
+    for (int i = 0; i < kTileRows / ROWS; ++i) c[i] = *reinterpret_cast<const word *>(codes + i * ROWS * 16);
 #pragma unroll
-    for (int s = 0; s < L::STEPS; ++s) c[s] = *reinterpret_cast<const word *>(tile + ln.byte(s));
-#pragma unroll
-    for (int s = 0; s < L::STEPS; ++s) {
-      const float sc = scale_of_code(scales[s] >> 8 * b & 255u);
+    for (int i = 0; i < kTileRows / ROWS; ++i) {
+      const int r = i * ROWS + r0;
+      const float sc = scale_of_code((uint32_t)__shfl((int)scales, g * kTileRows + r) >> 8 * b & 255u);
       u32x4_t v;
       if constexpr (sizeof(DT) == 2) {
-        v = e2m1x8_to_bf16(c[s], sc);
+        v = e2m1x8_to_bf16(c[i], sc);
       } else {
         typedef float f32x2_t __attribute__((ext_vector_type(2)));
-        const f32x2_t lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[s], sc, 0),
-                      hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[s], sc, 1);
+        const f32x2_t lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[i], sc, 0),
+                      hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[i], sc, 1);
         v = __builtin_bit_cast(u32x4_t, f32x4_t{lo[0], lo[1], hi[0], hi[1]});
       }
-      DT *row = w + (size_t)ln.row(s) * a.K;
-      if (ln.row(s) >= rows) continue;
-      if (k + L::PER <= a.K) {
-        __builtin_nontemporal_store(v, reinterpret_cast<mem *>(row + k));
-      } else {
-        const Chunk<DT> e = chunk_elems<DT>(v);
+      if (r < rows) {
+        DT *const row = w + (size_t)r * a.K;
+        if (k + PER <= a.K) {
+          mem *const p = reinterpret_cast<mem *>(row + k);
+          if constexpr (WHOLE) __builtin_nontemporal_store(v, p);
+          else *p = v;
+        } else {
+          const Chunk<DT> e = chunk_elems<DT>(v);
 #pragma unroll
-        for (int i = 0; i < L::PER; ++i)
-          if (k + i < a.K) row[k + i] = e.v[i];
+          for (int n = 0; n < PER; ++n)
+            if (k + n < a.K) row[k + n] = e.v[n];
+        }
       }
     }
   }
+}
+
+// A row at a time, so that a store is 1 KB of it: of rows that are no whole lines only the
+// first and last line of those are shared (16 x 11008 x 4090 bf16 400 us, by stores of 256 bytes
+// of four rows 633).  Two or four rows where a quad has few columns (44 x 3572 x 68 bf16 9 us, a
+// row at a time 17).
+template <bool WHOLE, typename DT>
+__global__ __launch_bounds__(kThreads) void k_dequant_fp4(Fp4WeightsArgs a) {
+  constexpr int PER = 16 / (int)sizeof(DT);
+  Quad q;
+  if (!quad_of(a, q)) return;
+  const uint32_t scales = quad_scales(a, q)[threadIdx.x % kWave];
+  const int width = (min(4 * kTileCols, a.K - q.k0) + PER - 1) / PER;  // lanes that a row takes
+  if (width > kWave / 2) dequant_quad<1, WHOLE, DT>(a, q, scales, width);
+  else if (width > kWave / 4) dequant_quad<2, WHOLE, DT>(a, q, scales, width);
+  else dequant_quad<4, WHOLE, DT>(a, q, scales, width);
 }
 
 template <typename K>
@@ -224,16 +247,32 @@ hipError_t launch(K kern, const Fp4WeightsArgs &a, hipStream_t st) {
   return launch_kernel(kern, dim3((unsigned)((quads + kWaves - 1) / kWaves)), dim3(kThreads), 0, st, a);
 }
 
+// The one of two kernels that the rows take (both, where a first call loads them).
+template <typename DT, typename K>
+hipError_t launch_rows(K whole, K other, const Fp4WeightsArgs &a, hipStream_t st) {
+  if (tl_resolve_only) {
+    const hipError_t e = launch(whole, a, st);
+    if (e != hipSuccess) return e;
+  }
+  return launch(whole_lines<DT>(a.K) && !tl_resolve_only ? whole : other, a, st);
+}
+template <typename DT> hipError_t quantize(const Fp4WeightsArgs &a, hipStream_t st) {
+  return launch_rows<DT>(k_quant_fp4<true, DT>, k_quant_fp4<false, DT>, a, st);
+}
+template <typename DT> hipError_t dequantize(const Fp4WeightsArgs &a, hipStream_t st) {
+  return launch_rows<DT>(k_dequant_fp4<true, DT>, k_dequant_fp4<false, DT>, a, st);
+}
+
 }  // namespace
 
 hipError_t launch_quantize_fp4(const Fp4WeightsArgs &a, bool bf16, hipStream_t st) {
-  return bf16 ? launch(k_quant_fp4<uint16_t>, a, st) : launch(k_quant_fp4<float>, a, st);
+  return bf16 ? quantize<uint16_t>(a, st) : quantize<float>(a, st);
 }
 
 hipError_t launch_pack_fp4(const Fp4WeightsArgs &a, hipStream_t st) { return launch(k_pack_fp4, a, st); }
 
 hipError_t launch_dequantize_fp4(const Fp4WeightsArgs &a, bool bf16, hipStream_t st) {
-  return bf16 ? launch(k_dequant_fp4<uint16_t>, a, st) : launch(k_dequant_fp4<float>, a, st);
+  return bf16 ? dequantize<uint16_t>(a, st) : dequantize<float>(a, st);
 }
 
 }  // namespace moelora
