@@ -417,7 +417,7 @@ MOELORA_API moelora_status moelora_route_backward(int32_t n_tokens, int32_t n_ex
  *   scales  [mats][NT][KQ][64][4] bytes; entry 16 g + r of (i, q) holds the
  *           scales of that group in tiles 4 q .. 4 q + 3
  * Limits (else MOELORA_ERR_UNSUPPORTED): 1 <= N <= 131072, 1 <= K <= 65536,
- * mats <= 65535, mats NT KQ < 2^26.
+ * mats <= 65535, mats NT KQ <= 2^26 - 4.
  *
  * From weights w [mats][N][K] of dtype: the scale of a group is the smallest
  * power of two 2^e >= max|w| / 6 (e >= -125), and w / 2^e, which is exact, is

@@ -127,7 +127,8 @@ moelora_status router_shape(int32_t T, int32_t E, int32_t k, int32_t dtype, Rout
   return MOELORA_OK;
 }
 
-constexpr long long kMaxTileFours = 1ll << 26;  // (a launch holds fewer than 2^32 threads)
+// A launch holds fewer than 2^32 threads; a workgroup of 256 makes four fours of tiles.
+constexpr long long kMaxTileFours = (1ll << 26) - 4;
 // Sizes of 4-bit weights; the pointers are left null.
 moelora_status fp4_shape(int32_t mats, int32_t N, int32_t K, Fp4WeightsArgs *a) {
   if (mats < 0) return MOELORA_ERR_INVALID_ARG;
@@ -138,7 +139,7 @@ moelora_status fp4_shape(int32_t mats, int32_t N, int32_t K, Fp4WeightsArgs *a) 
   a->NT = (N + 15) / 16;
   a->KB = (K + 127) / 128;
   a->KQ = (a->KB + 3) / 4;
-  return (long long)mats * a->NT * a->KQ < kMaxTileFours ? MOELORA_OK : MOELORA_ERR_UNSUPPORTED;
+  return (long long)mats * a->NT * a->KQ <= kMaxTileFours ? MOELORA_OK : MOELORA_ERR_UNSUPPORTED;
 }
 
 constexpr long long kMaxResults = 1ll << 34;  // (a thread of a tile makes eight and more)
