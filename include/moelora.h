@@ -445,9 +445,9 @@ MOELORA_API moelora_status moelora_dequantize_weights_fp4(int32_t n_mats, int32_
  * expert_start[e] <= m < expert_start[e+1],
  *   out[m][n] = sum_k x[m][k] w[e][n][k]
  * with x [M][K] and out [M][N] of dtype; products are exact, summed in float32
- * and rounded once.  (float32 rows meet the weights in three parts of eight
- * significant bits: a row with an infinity gives NaN where the sum would be
- * infinite.)  Rows outside every expert's range are left as they were.
+ * and rounded once (of float32 rows the products of three parts of eight
+ * significant bits each).  Rows outside every expert's range are left as they
+ * were.
  * expert_start = NULL with n_experts = 1: all rows (a dense product).
  * Entries of expert_start are clamped into [0, M]; they must not fall.
  * With MOELORA_FP4_SILU_MUL the weights of an expert are two matrices, gate

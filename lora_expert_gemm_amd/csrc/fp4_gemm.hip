@@ -27,17 +27,20 @@ namespace moelora {
 
 namespace {
 
-// Eight values of a row as MFMA operands whose sum they are.
+// Eight values of a row as MFMA operands whose sum they are.  INF: of infinities too,
+// which are their own upper part; without it inf - inf makes the lower ones NaN.  Every
+// contraction is made without it first (with it 2 to 3 % slower, one row 12 %), and where
+// a sum then is NaN once more with it.
 template <typename DT> struct Parts;
 template <> struct Parts<uint16_t> {
   static constexpr int kLoads = 1, kParts = 1;  // 16-byte loads for eight values
   u32x4_t p[1];
-  __device__ __forceinline__ static Parts of(const u32x4_t *v) { return {{v[0]}}; }
+  template <bool INF> __device__ __forceinline__ static Parts of(const u32x4_t *v) { return {{v[0]}}; }
 };
 template <> struct Parts<float> {
   static constexpr int kLoads = 2, kParts = 3;
   u32x4_t p[3];
-  __device__ __forceinline__ static Parts of(const u32x4_t *v) {
+  template <bool INF> __device__ __forceinline__ static Parts of(const u32x4_t *v) {
     Parts r;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -46,7 +49,8 @@ template <> struct Parts<float> {
       for (int j = 0; j < 2; ++j) {
         const uint32_t u = v[i / 2][i % 2 * 2 + j];
         const float f = __uint_as_float(u);
-        const float f1 = f - __uint_as_float(u & 0xffff0000u);  // exact
+        float f1 = f - __uint_as_float(u & 0xffff0000u);  // exact
+        if (INF && __builtin_isinf(f)) f1 = 0.f;
         const float f2 = f1 - __uint_as_float(__float_as_uint(f1) & 0xffff0000u);
         h[j] = u, m[j] = __float_as_uint(f1), l[j] = __float_as_uint(f2);
       }
@@ -58,6 +62,18 @@ template <> struct Parts<float> {
     return r;
   }
 };
+
+// Whether one of a lane's sums is NaN (or two are infinities of either sign).
+template <int N, int M> __device__ __forceinline__ bool some_nan(const f32x4_t (&acc)[N][M]) {
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int j = 0; j < M; ++j)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) s += acc[i][j][c];
+  return s != s;
+}
 
 // v shifted right by 0 <= n <= 16 bytes.
 __device__ __forceinline__ u32x4_t shift_right(u32x4_t v, int n) {
@@ -161,9 +177,7 @@ __global__ __launch_bounds__(W * kWave) void k_fp4_stream(Fp4GemmArgs a) {
   const int KB = a.KB, K = a.K, t0 = blockIdx.x * NT;
   const TileRows<HV, NT> tr(a, e, t0, lane);
   for (int m0 = lo + blockIdx.z * 16; m0 < hi; m0 += gridDim.z * 16) {
-    f32x4_t acc[A];
-#pragma unroll
-    for (int i = 0; i < A; ++i) acc[i] = f32x4_t{0, 0, 0, 0};
+    f32x4_t acc[1][A];
     const DT *const xrows = static_cast<const DT *>(a.x) + (size_t)m0 * K;
     const uint32_t row = (uint32_t)min(l16, hi - m0 - 1) * K;  // (rows past the last repeat it and are dropped)
     struct Slab {
@@ -176,31 +190,39 @@ __global__ __launch_bounds__(W * kWave) void k_fp4_stream(Fp4GemmArgs a) {
       for (int c = 0; c < 4; ++c) load8<DT>(xrows, row, b * kTileCols + g * kGroup + 8 * c, K, v.x[c]);
     };
     static_assert(W % 4 == 0, "a wave's slabs have one place in the scales' fours");
-    Slab v;
-    load(v, wave);
-    for (int b = wave; b < KB; b += W) {
-      if ((b + 1) * kTileCols > K) {
+    const auto contract = [&]<bool INF>() {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) fix8<DT>(b * kTileCols + g * kGroup + 8 * c, K, v.x[c]);
+      for (int i = 0; i < A; ++i) acc[0][i] = f32x4_t{0, 0, 0, 0};
+      Slab v;
+      load(v, wave);
+      for (int b = wave; b < KB; b += W) {
+        if ((b + 1) * kTileCols > K) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) fix8<DT>(b * kTileCols + g * kGroup + 8 * c, K, v.x[c]);
+        }
+        float s[A];
+#pragma unroll
+        for (int i = 0; i < A; ++i) s[i] = scale_of_code(v.w.s[i] >> 8 * (wave % 4) & 255u);  // (b % 4 is wave % 4)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          u32x4_t wv[A];
+#pragma unroll
+          for (int i = 0; i < A; ++i) wv[i] = e2m1x8_to_bf16(v.w.c[i][c], s[i]);
+          const Parts<DT> x = Parts<DT>::template of<INF>(v.x[c]);
+#pragma unroll
+          for (int q = 0; q < Parts<DT>::kParts; ++q)
+#pragma unroll
+            for (int i = 0; i < A; ++i) Mma<uint16_t>::step(acc[0][i], wv[i], x.p[q]);
+        }
+        load(v, b + W);
       }
-      float s[A];
-#pragma unroll
-      for (int i = 0; i < A; ++i) s[i] = scale_of_code(v.w.s[i] >> 8 * (wave % 4) & 255u);  // (b % 4 is wave % 4)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        u32x4_t wv[A];
-#pragma unroll
-        for (int i = 0; i < A; ++i) wv[i] = e2m1x8_to_bf16(v.w.c[i][c], s[i]);
-        const Parts<DT> x = Parts<DT>::of(v.x[c]);
-#pragma unroll
-        for (int q = 0; q < Parts<DT>::kParts; ++q)
-#pragma unroll
-          for (int i = 0; i < A; ++i) Mma<uint16_t>::step(acc[i], wv[i], x.p[q]);
-      }
-      load(v, b + W);
+    };
+    contract.template operator()<false>();
+    if constexpr (Parts<DT>::kParts > 1) {
+      if (__builtin_expect(__any(some_nan(acc)), 0)) contract.template operator()<true>();
     }
 #pragma unroll
-    for (int i = 0; i < A; ++i) red[wave][i][lane] = acc[i];
+    for (int i = 0; i < A; ++i) red[wave][i][lane] = acc[0][i];
     __syncthreads();
     // one wave per tile: the waves' sums in wave order
     for (int i = wave; i < NT; i += W) {
@@ -341,13 +363,13 @@ __global__ __launch_bounds__(KS * kGThreads, KS > 1 || WT * TT <= 4 ? 4 : WT * T
       load8<DT>(xrows, (uint32_t)r * K, b * kTileCols + c % 16 * 8, K, x.v[u]);
     }
   };
-  auto store_x = [&](Rows &x, int b, int s) {
+  auto store_x = [&]<bool INF>(Rows &x, int b, int s) {
     unsigned char *st = stages + s * STAGE;
 #pragma unroll
     for (int u = 0; u < XR; ++u) {
       const int c = u * kGThreads + tid;
       if ((b + 1) * kTileCols > K) fix8<DT>(b * kTileCols + c % 16 * 8, K, x.v[u]);
-      const P p = P::of(x.v[u]);
+      const P p = P::template of<INF>(x.v[u]);
 #pragma unroll
       for (int q = 0; q < P::kParts; ++q)
         *reinterpret_cast<u32x4_t *>(st + q * PLANE + slab_off(c / 16, c % 16)) = p.p[q];
@@ -355,15 +377,10 @@ __global__ __launch_bounds__(KS * kGThreads, KS > 1 || WT * TT <= 4 ? 4 : WT * T
   };
 
   f32x4_t acc[WT][TT];
-#pragma unroll
-  for (int i = 0; i < WT; ++i)
-#pragma unroll
-    for (int t = 0; t < TT; ++t) acc[i][t] = f32x4_t{0, 0, 0, 0};
-
   // The group's i-th slab with its weights in `w`, and what is loaded meanwhile: the
   // next one's weights into `wn`, its rows (and those of the one after).
   Rows x;
-  auto step = [&](int i, const Weights<WT> &w, Weights<WT> &wn) {
+  auto step = [&]<bool INF>(int i, const Weights<WT> &w, Weights<WT> &wn) {
     const int b = kg + i * KS, s = i & 1;
     if constexpr (DMA) {
       // this wave's tokens of b landed (the weights behind them may not have),
@@ -377,7 +394,7 @@ __global__ __launch_bounds__(KS * kGThreads, KS > 1 || WT * TT <= 4 ? 4 : WT * T
       __builtin_amdgcn_sched_barrier(0);
     } else {
       __syncthreads();  // slab b is stored, the one before read out
-      store_x(x, b + KS, s ^ 1);
+      store_x.template operator()<INF>(x, b + KS, s ^ 1);
       load_x(x, b + 2 * KS);
       load_weights<ONCE, HV, WH>(wn, tr, KB, b + KS);
     }
@@ -402,31 +419,47 @@ __global__ __launch_bounds__(KS * kGThreads, KS > 1 || WT * TT <= 4 ? 4 : WT * T
     }
   };
 
-  Weights<WT> wa, wb;
-  if constexpr (DMA) {
-    issue_x(kg, 0);
-    __builtin_amdgcn_sched_barrier(0);
-  } else {
-    load_x(x, kg);
+  const auto contract = [&]<bool INF>() {
+#pragma unroll
+    for (int i = 0; i < WT; ++i)
+#pragma unroll
+      for (int t = 0; t < TT; ++t) acc[i][t] = f32x4_t{0, 0, 0, 0};
+    Weights<WT> wa, wb;
+    if constexpr (DMA) {
+      issue_x(kg, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    } else {
+      load_x(x, kg);
+    }
+    load_weights<ONCE, HV, WH>(wa, tr, KB, kg);
+    if constexpr (!DMA) {
+      store_x.template operator()<INF>(x, kg, 0);
+      load_x(x, kg + KS);
+    }
+    // (every group makes as many steps, one barrier each; slabs past the last are zeros)
+    const int steps = (KB + KS - 1) / KS;
+    int i = 0;
+    for (; i + 1 < steps; i += 2) {
+      step.template operator()<INF>(i, wa, wb);
+      step.template operator()<INF>(i + 1, wb, wa);
+    }
+    if (i < steps) step.template operator()<INF>(i, wa, wb);
+    __builtin_amdgcn_s_waitcnt(0x0f70);  // no load of this workgroup outlives it
+  };
+  __shared__ int again;  // (cleared before the first step's barrier, set behind the last one's)
+  if (P::kParts > 1 && threadIdx.x == 0) again = 0;
+  contract.template operator()<false>();
+  if (P::kParts > 1 && some_nan(acc)) again = 1;
+  if constexpr (P::kParts > 1 || KS > 1) __syncthreads();  // no stage is written again while it is read
+  if constexpr (P::kParts > 1) {
+    if (__builtin_expect(__builtin_amdgcn_readfirstlane(again), 0)) {
+      contract.template operator()<true>();
+      __syncthreads();
+    }
   }
-  load_weights<ONCE, HV, WH>(wa, tr, KB, kg);
-  if constexpr (!DMA) {
-    store_x(x, kg, 0);
-    load_x(x, kg + KS);
-  }
-  // (every group makes as many steps, one barrier each; slabs past the last are zeros)
-  const int steps = (KB + KS - 1) / KS;
-  int i = 0;
-  for (; i + 1 < steps; i += 2) {
-    step(i, wa, wb);
-    step(i + 1, wb, wa);
-  }
-  if (i < steps) step(i, wa, wb);
-  __builtin_amdgcn_s_waitcnt(0x0f70);  // no load of this workgroup outlives it
 
   if constexpr (KS > 1) {
     f32x4_t *const sums = reinterpret_cast<f32x4_t *>(smem) + tid;
-    __syncthreads();
     if (kg > 0) {
 #pragma unroll
       for (int i = 0; i < WT; ++i)
