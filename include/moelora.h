@@ -447,9 +447,8 @@ MOELORA_API moelora_status moelora_dequantize_weights_fp4(int32_t n_mats, int32_
  * with x [M][K] and out [M][N] of dtype; products are exact, summed in float32
  * and rounded once (of float32 rows the products of three parts of eight
  * significant bits each, the last a multiple of 2^-133: an element below 2^-110
- * counts as cut to such a multiple, by less than 2^-133; K < 4: float32
- * products, added by fma).  Rows outside every expert's range are left as they
- * were.
+ * counts as cut to such a multiple; whole where K < 4).  Rows outside every
+ * expert's range are left as they were.
  * expert_start = NULL with n_experts = 1: all rows (a dense product).
  * Entries of expert_start are clamped into [0, M]; they must not fall.
  * With MOELORA_FP4_SILU_MUL the weights of an expert are two matrices, gate

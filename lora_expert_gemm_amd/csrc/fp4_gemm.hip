@@ -13,7 +13,8 @@
 // column side).  A lane holds 32 neighbouring columns of its weight row, the
 // i-th instruction takes the eight from 8 i on, and the tokens' operand is read
 // to match.  float32 rows are cut into three bf16 parts (the upper, middle and
-// lower eight bits of the significand: their sum is the value itself), and
+// lower eight bits of the significand: their sum is the value itself from 2^-110 on,
+// below that the value cut to a multiple of 2^-133, bf16's smallest step), and
 // every part meets the weights in turn; sums are float32 throughout.
 #include <algorithm>
 
