@@ -35,9 +35,9 @@ FLAGS = [
 # (s_waitcnt vmcnt with a fixed immediate): a scratch spill reload is a
 # vector load too, so every kernel of these must use no scratch memory.
 COUNTED_WAITS = ("expert_gemm.hip", "tiled_gemm.hip", "fp8_gemm.hip", "fp4_gemm.hip")
-# The device assembly of the streaming GEMMs is kept for the CPU test that
-# checks the compiled weight-ring loops against their wait counts.
-ASM_SOURCES = ("expert_gemm.hip",)
+# The device assembly of the streaming GEMMs and of the 4-bit product is kept for
+# the CPU tests that check the compiled loops against their wait counts.
+ASM_SOURCES = ("expert_gemm.hip", "fp4_gemm.hip")
 _NOISE = "is not a recognized feature for this target"  # host pass, packed-fp32 flag
 _REMARK = re.compile(r"remark:\s+(Function Name|ScratchSize \[bytes/lane\]|VGPRs Spill|"
                      r"SGPRs Spill|VGPRs|AGPRs|Occupancy \[waves/SIMD\]|"
