@@ -416,6 +416,7 @@ MOELORA_API moelora_status moelora_route_backward(int32_t n_tokens, int32_t n_ex
  *           lower column in the low half
  *   scales  [mats][NT][KQ][64][4] bytes; entry 16 g + r of (i, q) holds the
  *           scales of that group in tiles 4 q .. 4 q + 3
+ * (1024 mats NT KB bytes and 256 mats NT KQ).
  * Limits (else MOELORA_ERR_UNSUPPORTED): 1 <= N <= 131072, 1 <= K <= 65536,
  * mats <= 65535, mats NT KQ <= 2^26 - 4.
  *

@@ -430,15 +430,16 @@ def moelora_route_backward(n_tokens, n_experts, top_k, dtype, flags, logits, tok
         _buf(dlogits, n, dt, dev, "dlogits"), st), "moelora_route_backward")
 
 
-def _fp4_bytes(n_mats, rows, width):
-    """Bytes of the codes and of the scales of 4-bit weights."""
+def fp4_weight_bytes(n_mats, rows, width):
+    """-> bytes of the codes and of the scales of n_mats 4-bit weight matrices of
+    rows x width (an expert's gate and up are two)."""
     tiles, kb = n_mats * ((rows + 15) // 16), (width + 127) // 128
     return tiles * kb * 1024, tiles * ((kb + 3) // 4) * 256
 
 
 def moelora_quantize_weights_fp4(n_mats, rows, width, dtype, w, codes, scales, stream=None):
     st, dev = _where(stream)
-    nc, ns = _fp4_bytes(n_mats, rows, width)
+    nc, ns = fp4_weight_bytes(n_mats, rows, width)
     _check(_lib.moelora_quantize_weights_fp4(
         n_mats, rows, width, dtype, _buf(w, n_mats * rows * width, _dt(dtype), dev, "w"),
         _buf(codes, nc, _BYTE, dev, "codes"), _buf(scales, ns, _BYTE, dev, "scales"), st),
@@ -447,7 +448,7 @@ def moelora_quantize_weights_fp4(n_mats, rows, width, dtype, w, codes, scales, s
 
 def moelora_pack_weights_fp4(n_mats, rows, width, row_codes, row_scales, codes, scales, stream=None):
     st, dev = _where(stream)
-    nc, ns = _fp4_bytes(n_mats, rows, width)
+    nc, ns = fp4_weight_bytes(n_mats, rows, width)
     _check(_lib.moelora_pack_weights_fp4(
         n_mats, rows, width, _buf(row_codes, n_mats * rows * ((width + 1) // 2), _BYTE, dev, "row_codes"),
         _buf(row_scales, n_mats * rows * ((width + 31) // 32), _BYTE, dev, "row_scales"),
@@ -457,7 +458,7 @@ def moelora_pack_weights_fp4(n_mats, rows, width, row_codes, row_scales, codes, 
 
 def moelora_dequantize_weights_fp4(n_mats, rows, width, dtype, codes, scales, w, stream=None):
     st, dev = _where(stream)
-    nc, ns = _fp4_bytes(n_mats, rows, width)
+    nc, ns = fp4_weight_bytes(n_mats, rows, width)
     _check(_lib.moelora_dequantize_weights_fp4(
         n_mats, rows, width, dtype, _buf(codes, nc, _BYTE, dev, "codes"),
         _buf(scales, ns, _BYTE, dev, "scales"), _buf(w, n_mats * rows * width, _dt(dtype), dev, "w"), st),
@@ -467,7 +468,7 @@ def moelora_dequantize_weights_fp4(n_mats, rows, width, dtype, codes, scales, w,
 def moelora_fp4_gemm(n_rows, n_out, width, n_experts, dtype, flags, x, expert_start, w_codes, w_scales,
                      out, stream=None):
     st, dev = _where(stream)
-    nc, ns = _fp4_bytes(n_experts * (2 if flags & FP4_SILU_MUL else 1), n_out, width)
+    nc, ns = fp4_weight_bytes(n_experts * (2 if flags & FP4_SILU_MUL else 1), n_out, width)
     dt = _dt(dtype)
     _check(_lib.moelora_fp4_gemm(
         n_rows, n_out, width, n_experts, dtype, flags, _buf(x, n_rows * width, dt, dev, "x"),
