@@ -569,22 +569,27 @@ long long workgroups(const Fp4GemmArgs &a, int GM, int tiles) {
 }
 
 // Which kernel, by the mean rows of an expert and by how many workgroups it leaves
-// (256 CUs).  us on one card; "g": by tokens, 32 experts, top-4, 2880 -> 2 x 2880 with
+// (256 CUs); the host knows no more of the rows than their mean, so rows that crowd on few
+// experts may take a slower one: 1024 rows, 2880 -> 2 x 2880 with SILU, bf16, are streamed for
+// 256 experts, 348 us of even rows, 242 with all on two experts (41 by 4x4), where at most four
+// workgroups a column group go through an expert's groups of 16 rows and its weights each time.
+// us on one card; "g": by tokens, 32 experts, top-4, 2880 -> 2 x 2880 with
 // SILU, bf16; "d": by rows, one expert, 4096 -> 11008.
 //   few rows, many experts: four weight tiles a workgroup without LDS against tiles whose
 //     tokens go through it: g16 37 / 43 (4x2), g64 57 / 48, g128 96 / 62 (16 tokens of
-//     float32 58 / 49, by 4x1: they stay with tiles)
+//     float32 58 / 51, by 4x1: they stay with tiles)
 //   few rows, few workgroups: two weight tiles and eight waves on the contraction: d1 7.1
 //     (four tiles and waves 8.6, split tiles 7.8)
 //   little work: tiles with the contraction split over four groups of waves.  1x1: d16 8.0
 //     (streamed 9.5 to 12, not split 17), 16 experts x 8 rows 4000 -> 500 8.0 (10.8), d64 16.2;
 //     2x2: d64 13.0 (not split 20), 256 rows 4096 -> 4096 13.4 (17.4), 1000 rows of 8 experts
-//     8000 -> 300 24 (29 by 1x1); float32 4x1: d64 23 (37).  Its sixteen
-//     waves fill a CU: with more workgroups than CUs 2300 rows of 5 experts 1024 -> 446 12.5
-//     (9.0), 3735 float32 rows of 94 948 -> 98 19.7 (14.1; with four column groups and more
-//     the rows come from caches, 1024 rows of 8 2048 -> 625 14.6 (17.1))
-//   float32: 4x1 against 4x2, 21 rows an expert of 128, 2050 -> 771 48 / 58; 128 rows an
-//     expert of 32 374 / 351
+//     8000 -> 300 24 (29 by 1x1); float32 4x1: d64 23 (30).  Its sixteen
+//     waves fill a CU: with more workgroups than CUs 2300 rows of 5 experts 1024 -> 446 12.6
+//     (7.6 by 2x2 by DMA, which they take, 9.0 by 4x2), 3735 float32 rows of 94 948 -> 98 19.7
+//     (14.3; with four column groups and more the rows come from caches, 1024 rows of 8
+//     2048 -> 625 14.6 (17.1))
+//   float32: 4x1 against 4x2, 21 rows an expert of 128, 2050 -> 771 49 / 59; 128 rows an
+//     expert of 32 359 / 341
 //   bf16, a few workgroups a CU, rows straight into LDS: 2x2 against 4x2: 1024 rows of 8
 //     2048 -> 1250 11.4 / 13.7, -> 2600 17.1 / 19.9, -> 6000 34.5 / 30.9 (4x4)
 //   bf16: 4x2 past the caches or through them g64 47 / 54, g256 79 / 78; 4x4 against 4x2
